@@ -11,6 +11,9 @@
 #include <vector>
 
 #include "common.cuh"
+#include "pages.cuh"
+#include "prefix.cuh"
+#include "ragged.cuh"
 
 namespace kvq {
 cudaError_t launch_energy(const void* k, int dtype, int64_t n_tokens, int n_kv,
@@ -873,6 +876,215 @@ int kvq_paged_append_decode(const kvq_cfg* cfg, const void* const* plans_dev, co
   return append_decode_impl(cfg, plans_dev, k_dev, v_dev, kv_dtype, n_new, cm, len_dev, cap,
                             batch, max_len, q_dev, q_dtype, n_q_heads, out_dev, ws_dev, ws_bytes,
                             step_flags, rope_base, status_dev, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Page checks of the calls that take a pool without a block table; tokens per
+// page as a shift.
+int page_shape(int64_t n_pages, int32_t page_tiles, int* shift) {
+  if (page_tiles < 1 || page_tiles > (1 << 20) || (page_tiles & (page_tiles - 1)))
+    return fail(KVQ_ERR_ARG, "page_tiles %d (a power of two, 1..2^20)", page_tiles);
+  if (n_pages < 1 || n_pages > 0x7FFFFFFF)
+    return fail(KVQ_ERR_ARG, "n_pages %lld", (long long)n_pages);
+  *shift = 0;
+  while ((1 << *shift) < page_tiles * kTile) ++*shift;
+  return KVQ_OK;
+}
+
+int prefix_impl(const kvq_cfg* cfg, const void* const* plans_dev, const CacheMap& pre,
+                const int32_t* prefix_len_dev, const int32_t* group_start_dev, int n_prefixes,
+                int64_t max_prefix_len, const CacheMap& own, const int32_t* len_dev, int batch,
+                int64_t max_len, const void* q_dev, int q_dtype, int n_q_heads, void* out_dev,
+                int out_dtype, void* ws_dev, size_t ws_bytes, uint32_t* status_dev,
+                kvq_stream_t stream) {
+  int rc = check_cfg(cfg);
+  if (rc) return rc;
+  if (!plans_dev || !(pre.caches || pre.table) || !(own.caches || own.table) ||
+      !prefix_len_dev || !group_start_dev || !len_dev || !q_dev || !out_dev || !ws_dev ||
+      !status_dev)
+    return fail(KVQ_ERR_ARG, "null device pointer");
+  if (!dtype_ok(q_dtype)) return fail(KVQ_ERR_ARG, "q_dtype %d", q_dtype);
+  if (!dtype_ok(out_dtype)) return fail(KVQ_ERR_ARG, "out_dtype %d", out_dtype);
+  if (batch < 1 || batch > 65535) return fail(KVQ_ERR_ARG, "batch %d", batch);
+  if (n_prefixes < 1 || n_prefixes > kPfxMaxGroups)
+    return fail(KVQ_ERR_ARG, "n_prefixes %d not in 1..%d", n_prefixes, kPfxMaxGroups);
+  if (max_len < 1 || max_len > 0x7FFFFFFF || max_prefix_len < 1 || max_prefix_len > 0x7FFFFFFF)
+    return fail(KVQ_ERR_ARG, "max_len %lld / max_prefix_len %lld", (long long)max_len,
+                (long long)max_prefix_len);
+  if (n_q_heads < 1 || n_q_heads % cfg->n_kv_heads != 0 || n_q_heads / cfg->n_kv_heads > 16)
+    return fail(KVQ_ERR_ARG, "n_q_heads %d vs n_kv_heads %d", n_q_heads, cfg->n_kv_heads);
+  if (reinterpret_cast<uintptr_t>(ws_dev) & 255)
+    return fail(KVQ_ERR_ARG, "prefix workspace not 256-byte aligned");
+  if (reinterpret_cast<uintptr_t>(out_dev) & 15)
+    return fail(KVQ_ERR_ARG, "out not 16-byte aligned");
+  const size_t need = kvq_prefix_decode_workspace_bytes(cfg, batch, n_q_heads, n_prefixes);
+  if (ws_bytes < need)
+    return fail(KVQ_ERR_WORKSPACE, "prefix workspace %zu < %zu", ws_bytes, need);
+  PrefixArgs a;
+  a.plans = reinterpret_cast<const Plan* const*>(plans_dev);
+  a.pre = pre;
+  a.pre_len = prefix_len_dev;
+  a.group_start = group_start_dev;
+  a.n_groups = n_prefixes;
+  a.max_pre = max_prefix_len;
+  a.own = own;
+  a.len = len_dev;
+  a.max_len = max_len;
+  a.batch = batch;
+  a.n_q = n_q_heads;
+  a.n_kv = cfg->n_kv_heads;
+  a.bits_k = cfg->bits_k;
+  a.bits_v = cfg->bits_v;
+  a.q = q_dev;
+  a.q_dtype = q_dtype;
+  a.out = out_dev;
+  a.out_dtype = out_dtype;
+  a.status = status_dev;
+  cudaError_t e = launch_prefix_decode(a, ws_dev, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "prefix_decode_attn");
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------- page bookkeeping, ragged batches
+size_t kvq_pages_assign_workspace_bytes(int batch) {
+  if (batch < 1 || batch > 65535) return 0;
+  return pages_workspace_bytes(batch);
+}
+
+int kvq_pages_assign(const kvq_page_state* state, const int32_t* len_dev,
+                     const int32_t* n_new_dev, int batch, int64_t n_slots, int32_t* cu_dev,
+                     int64_t* slot_dev, int32_t* pos_dev, void* ws_dev, size_t ws_bytes,
+                     uint32_t* status_dev, kvq_stream_t stream) {
+  if (!state || !state->block_table || !state->held || !state->free_ids || !state->free_ring)
+    return fail(KVQ_ERR_ARG, "null page state");
+  if (!len_dev || !n_new_dev || !cu_dev || !ws_dev || !status_dev)
+    return fail(KVQ_ERR_ARG, "null device pointer");
+  if (batch < 1 || batch > 65535) return fail(KVQ_ERR_ARG, "batch %d", batch);
+  if (n_slots < 0 || n_slots > 0x7FFFFFFF)
+    return fail(KVQ_ERR_ARG, "n_slots %lld", (long long)n_slots);
+  if (n_slots > 0 && !slot_dev) return fail(KVQ_ERR_ARG, "null slot array");
+  PagesParams p;
+  int rc = page_shape(state->n_pages, state->page_tiles, &p.span_shift);
+  if (rc) return rc;
+  p.span = state->page_tiles * kTile;
+  if (state->max_pages < 1 || (int64_t)state->max_pages * p.span > 0x7FFFFFFF)
+    return fail(KVQ_ERR_ARG, "max_pages %d", state->max_pages);
+  if (reinterpret_cast<uintptr_t>(ws_dev) & 15)
+    return fail(KVQ_ERR_ARG, "pages workspace not 16-byte aligned");
+  if (ws_bytes < pages_workspace_bytes(batch))
+    return fail(KVQ_ERR_WORKSPACE, "pages workspace %zu < %zu", ws_bytes,
+                pages_workspace_bytes(batch));
+  p.table = state->block_table;
+  p.held = state->held;
+  p.free_ids = state->free_ids;
+  p.ring = state->free_ring;
+  p.n_pages = state->n_pages;
+  p.max_pages = state->max_pages;
+  p.len = len_dev;
+  p.n_new = n_new_dev;
+  p.batch = batch;
+  p.n_slots = n_slots;
+  p.cu = cu_dev;
+  p.slots = slot_dev;
+  p.pos = pos_dev;
+  p.status = status_dev;
+  cudaError_t e = launch_pages_assign(p, ws_dev, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "pages_assign");
+  return KVQ_OK;
+}
+
+int kvq_paged_append_ragged(const kvq_cfg* cfg, const void* const* plans_dev, const void* k_dev,
+                            const void* v_dev, int dtype, int64_t n_rows, const int32_t* cu_dev,
+                            const int64_t* slot_dev, int batch, void* pool, int64_t n_pages,
+                            int32_t page_tiles, int32_t* len_dev, double rope_base,
+                            uint32_t* status_dev, kvq_stream_t stream) {
+  int rc = check_cfg(cfg);
+  if (rc) return rc;
+  RaggedParams p;
+  rc = page_shape(n_pages, page_tiles, &p.span_shift);
+  if (rc) return rc;
+  if (!plans_dev || !cu_dev || !pool || !len_dev || !status_dev)
+    return fail(KVQ_ERR_ARG, "null device pointer");
+  if (!dtype_ok(dtype)) return fail(KVQ_ERR_ARG, "dtype %d", dtype);
+  if (batch < 1 || batch > 65535) return fail(KVQ_ERR_ARG, "batch %d", batch);
+  if (n_rows < 0 || n_rows > 0x7FFFFFFF)
+    return fail(KVQ_ERR_ARG, "n_rows %lld", (long long)n_rows);
+  if (reinterpret_cast<uintptr_t>(pool) & 15)
+    return fail(KVQ_ERR_ARG, "page pool not 16-byte aligned");
+  p.rope = rope_base != 0.0 ? 1 : 0;
+  for (int j = 0; j < 64; ++j) p.theta[j] = 0.0;
+  if (p.rope && !rope_thetas(rope_base, p.theta))
+    return fail(KVQ_ERR_ARG, "rope_base %g", rope_base);
+  if (n_rows == 0) return KVQ_OK;
+  if (!k_dev || !v_dev || !slot_dev) return fail(KVQ_ERR_ARG, "null k/v/slot pointer");
+  p.plans = reinterpret_cast<const Plan* const*>(plans_dev);
+  p.k = k_dev;
+  p.v = v_dev;
+  p.dtype = dtype;
+  p.cu = cu_dev;
+  p.slots = slot_dev;
+  p.batch = batch;
+  p.n_kv = cfg->n_kv_heads;
+  p.n_rows = n_rows;
+  p.pool = static_cast<uint8_t*>(pool);
+  p.n_pages = n_pages;
+  p.page_bytes = (int64_t)kvq_page_bytes(cfg, page_tiles);
+  p.span = page_tiles * kTile;
+  p.len = len_dev;
+  p.tile_bytes = tile_bytes(cfg->bits_k, cfg->bits_v);
+  p.status = status_dev;
+  cudaError_t e = launch_append_ragged(p, cfg->bits_v, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_append_ragged");
+  return KVQ_OK;
+}
+
+// ------------------------------------------------------------ shared prefixes
+size_t kvq_prefix_decode_workspace_bytes(const kvq_cfg* cfg, int batch, int n_q_heads,
+                                         int n_prefixes) {
+  if (check_cfg(cfg) != KVQ_OK || batch < 1 || batch > 65535 || n_prefixes < 1 ||
+      n_prefixes > kPfxMaxGroups || n_q_heads < 1 || n_q_heads % cfg->n_kv_heads != 0 ||
+      n_q_heads / cfg->n_kv_heads > 16)
+    return 0;
+  return prefix_workspace_bytes(batch, n_q_heads, cfg->n_kv_heads, n_prefixes);
+}
+
+int kvq_prefix_decode_attn(const kvq_cfg* cfg, const void* const* plans_dev,
+                           const void* const* prefix_cache_dev, const int32_t* prefix_len_dev,
+                           const int32_t* group_start_dev, int n_prefixes, int64_t max_prefix_len,
+                           const void* const* cache_dev, const int32_t* len_dev, int batch,
+                           int64_t max_len, const void* q_dev, int q_dtype, int n_q_heads,
+                           void* out_dev, int out_dtype, void* ws_dev, size_t ws_bytes,
+                           uint32_t* status_dev, kvq_stream_t stream) {
+  return prefix_impl(cfg, plans_dev, contiguous_map(prefix_cache_dev), prefix_len_dev,
+                     group_start_dev, n_prefixes, max_prefix_len, contiguous_map(cache_dev),
+                     len_dev, batch, max_len, q_dev, q_dtype, n_q_heads, out_dev, out_dtype,
+                     ws_dev, ws_bytes, status_dev, stream);
+}
+
+int kvq_paged_prefix_decode_attn(const kvq_cfg* cfg, const void* const* plans_dev,
+                                 const kvq_pages* prefix_pages, const int32_t* prefix_len_dev,
+                                 const int32_t* group_start_dev, int n_prefixes,
+                                 int64_t max_prefix_len, const kvq_pages* pages,
+                                 const int32_t* len_dev, int batch, int64_t max_len,
+                                 const void* q_dev, int q_dtype, int n_q_heads, void* out_dev,
+                                 int out_dtype, void* ws_dev, size_t ws_bytes,
+                                 uint32_t* status_dev, kvq_stream_t stream) {
+  CacheMap pre, own;
+  int64_t cap = 0;
+  int rc = paged_map(cfg, prefix_pages, &pre, &cap);
+  if (rc) return rc;
+  rc = paged_map(cfg, pages, &own, &cap);
+  if (rc) return rc;
+  return prefix_impl(cfg, plans_dev, pre, prefix_len_dev, group_start_dev, n_prefixes,
+                     max_prefix_len, own, len_dev, batch, max_len, q_dev, q_dtype, n_q_heads,
+                     out_dev, out_dtype, ws_dev, ws_bytes, status_dev, stream);
 }
 
 }  // extern "C"

@@ -66,6 +66,16 @@ class Pages(ctypes.Structure):
                 ("max_pages", ctypes.c_int32)]
 
 
+class PageState(ctypes.Structure):
+    """kvq_page_state: block table [batch][max_pages] and pages held [batch]
+    (int32), ring of free page ids (int32 [n_pages]) with its head and count
+    (int64 [2]), all on the device."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("free_ids", ctypes.c_void_p), ("free_ring", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page_tiles", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
 _vp, _sz, _i32, _i64, _u32p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64, \
     ctypes.c_void_p
 _SIGS = {
@@ -121,6 +131,19 @@ _SIGS = {
     "kvq_window_decode_workspace_bytes": (_sz, [ctypes.POINTER(Cfg), _i32, _i32, _i64]),
     "kvq_decode_attn_window": (_i32, [ctypes.POINTER(Cfg), _vp, _vp, _vp, _vp, _vp, _i32, _i32,
                                       _i64, _vp, _i32, _i32, _vp, _vp, _sz, _vp, _vp]),
+    "kvq_pages_assign_workspace_bytes": (_sz, [_i32]),
+    "kvq_pages_assign": (_i32, [ctypes.POINTER(PageState), _vp, _vp, _i32, _i64, _vp, _vp, _vp,
+                                _vp, _sz, _vp, _vp]),
+    "kvq_paged_append_ragged": (_i32, [ctypes.POINTER(Cfg), _vp, _vp, _vp, _i32, _i64, _vp, _vp,
+                                       _i32, _vp, _i64, _i32, _vp, ctypes.c_double, _vp, _vp]),
+    "kvq_prefix_decode_workspace_bytes": (_sz, [ctypes.POINTER(Cfg), _i32, _i32, _i32]),
+    "kvq_prefix_decode_attn": (_i32, [ctypes.POINTER(Cfg), _vp, _vp, _vp, _vp, _i32, _i64, _vp,
+                                      _vp, _i32, _i64, _vp, _i32, _i32, _vp, _i32, _vp, _sz, _vp,
+                                      _vp]),
+    "kvq_paged_prefix_decode_attn": (_i32, [ctypes.POINTER(Cfg), _vp, ctypes.POINTER(Pages), _vp,
+                                            _vp, _i32, _i64, ctypes.POINTER(Pages), _vp, _i32,
+                                            _i64, _vp, _i32, _i32, _vp, _i32, _vp, _sz, _vp,
+                                            _vp]),
     "kvq_append_decode_window": (_i32, [ctypes.POINTER(Cfg), _vp, _vp, _vp, _i32, _i32, _vp, _vp,
                                         _i64, _vp, _vp, _i32, _i32, _i64, _vp, _i32, _i32, _vp,
                                         _vp, _sz, _i32, _vp, _vp]),
@@ -451,3 +474,113 @@ def decode_attn_window(cfg, plan_ptrs, cache_ptrs, lens, win_ptrs, wlens, R, max
                                         max_len, _ptr(q), _dtype_code(q), n_q, _ptr(out),
                                         _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
                                         _stream()))
+
+
+# ------------------------------------------ page bookkeeping, ragged batches
+def _need(t, name, dtype, *shape):
+    """Refuse a tensor that is not a contiguous device array of this type and
+    shape (None: any size): the library only sees its address."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.dim() != len(shape) or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise KVQError(ERR_ARG, f"{name}: contiguous {dtype} device tensor of shape {shape}, not "
+                                f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def make_page_state(table, held, free_ids, free_ring, page_tiles):
+    """kvq_page_state over device tensors: table int32 [batch, max_pages],
+    held int32 [batch], free_ids int32 [n_pages], free_ring int64 [2]."""
+    import torch
+    _need(table, "table", torch.int32, None, None)
+    _need(held, "held", torch.int32, table.shape[0])
+    _need(free_ids, "free_ids", torch.int32, None)
+    _need(free_ring, "free_ring", torch.int64, 2)
+    return PageState(table.data_ptr(), held.data_ptr(), free_ids.data_ptr(), free_ring.data_ptr(),
+                     free_ids.shape[0], page_tiles, table.shape[1])
+
+
+def pages_assign_workspace_bytes(batch) -> int:
+    return lib().kvq_pages_assign_workspace_bytes(batch)
+
+
+def pages_assign(state, lens, n_new, cu, slots, pos, ws, status):
+    """Pages and slots of a step: n_new int32 [batch] tokens after lengths lens.
+    Fills cu int32 [batch + 1], slots int64 [n_slots], pos int32 [n_slots] (or
+    None) and moves pages between the rows and the free ring."""
+    import torch
+    batch = lens.shape[0]
+    _need(lens, "lens", torch.int32, batch)
+    _need(n_new, "n_new", torch.int32, batch)
+    _need(cu, "cu", torch.int32, batch + 1)
+    _need(slots, "slots", torch.int64, None)
+    if pos is not None:
+        _need(pos, "pos", torch.int32, slots.shape[0])
+    _check(lib().kvq_pages_assign(ctypes.byref(state), lens.data_ptr(), n_new.data_ptr(), batch,
+                                  slots.shape[0], cu.data_ptr(), slots.data_ptr(), _ptr(pos),
+                                  ws.data_ptr(), ws.numel() * ws.element_size(),
+                                  status.data_ptr(), _stream()))
+
+
+def paged_append_ragged(cfg, plan_ptrs, k, v, cu, slots, pool, n_pages, page_tiles, lens, status,
+                        rope_base=0.0):
+    """Quantize-append the packed rows k, v [n_rows, n_kv, 128] into the slots
+    of pages_assign (rope_base > 1: pre-RoPE keys) and advance lens."""
+    import torch
+    batch, n_rows = lens.shape[0], k.shape[0]
+    _need(k, "k", k.dtype, None, cfg.n_kv_heads, 128)
+    _need(v, "v", k.dtype, n_rows, cfg.n_kv_heads, 128)
+    _need(cu, "cu", torch.int32, batch + 1)
+    _need(slots, "slots", torch.int64, None)
+    _need(lens, "lens", torch.int32, batch)
+    if slots.shape[0] < n_rows or pool.numel() * pool.element_size() < \
+            n_pages * page_bytes(cfg, page_tiles):
+        raise KVQError(ERR_ARG, f"{slots.shape[0]} slots for {n_rows} rows, pool of "
+                                f"{pool.numel() * pool.element_size()} bytes")
+    _check(lib().kvq_paged_append_ragged(ctypes.byref(cfg), plan_ptrs.data_ptr(), k.data_ptr(),
+                                         v.data_ptr(), _dtype_code(k), n_rows, cu.data_ptr(),
+                                         slots.data_ptr(), batch, pool.data_ptr(), n_pages,
+                                         page_tiles, lens.data_ptr(), float(rope_base),
+                                         status.data_ptr(), _stream()))
+
+
+# ------------------------------------------------------------ shared prefixes
+def prefix_decode_workspace_bytes(cfg, batch, n_q_heads, n_prefixes) -> int:
+    return lib().kvq_prefix_decode_workspace_bytes(ctypes.byref(cfg), batch, n_q_heads,
+                                                   n_prefixes)
+
+
+def _prefix_args(prefix_lens, group_start, lens, q, out):
+    import torch
+    batch, n_prefixes = lens.shape[0], prefix_lens.shape[0]
+    _need(prefix_lens, "prefix_lens", torch.int32, n_prefixes)
+    _need(group_start, "group_start", torch.int32, n_prefixes + 1)
+    _need(lens, "lens", torch.int32, batch)
+    _need(q, "q", q.dtype, batch, None, 128)
+    _need(out, "out", out.dtype, batch, q.shape[1], 128)
+    return batch, n_prefixes
+
+
+def prefix_decode_attn(cfg, plan_ptrs, prefix_ptrs, prefix_lens, group_start, max_prefix_len,
+                       cache_ptrs, lens, max_len, q, out, ws, status):
+    """Decode q [batch, n_q, 128] into out (bf16, fp16 or fp32) over each
+    group's shared prefix cache (sequences group_start[g] .. group_start[g + 1]
+    - 1 share prefix g) and each sequence's own cache."""
+    batch, n_prefixes = _prefix_args(prefix_lens, group_start, lens, q, out)
+    _check(lib().kvq_prefix_decode_attn(
+        ctypes.byref(cfg), plan_ptrs.data_ptr(), prefix_ptrs.data_ptr(), prefix_lens.data_ptr(),
+        group_start.data_ptr(), n_prefixes, max_prefix_len, cache_ptrs.data_ptr(),
+        lens.data_ptr(), batch, max_len, q.data_ptr(), _dtype_code(q), q.shape[1],
+        out.data_ptr(), _dtype_code(out), ws.data_ptr(), ws.numel() * ws.element_size(),
+        status.data_ptr(), _stream()))
+
+
+def paged_prefix_decode_attn(cfg, plan_ptrs, prefix_pages, prefix_lens, group_start,
+                             max_prefix_len, pages, lens, max_len, q, out, ws, status):
+    """prefix_decode_attn over paged caches (the prefixes' block-table rows in
+    prefix_pages, the sequences' in pages)."""
+    batch, n_prefixes = _prefix_args(prefix_lens, group_start, lens, q, out)
+    _check(lib().kvq_paged_prefix_decode_attn(
+        ctypes.byref(cfg), plan_ptrs.data_ptr(), ctypes.byref(prefix_pages),
+        prefix_lens.data_ptr(), group_start.data_ptr(), n_prefixes, max_prefix_len,
+        ctypes.byref(pages), lens.data_ptr(), batch, max_len, q.data_ptr(), _dtype_code(q),
+        q.shape[1], out.data_ptr(), _dtype_code(out), ws.data_ptr(),
+        ws.numel() * ws.element_size(), status.data_ptr(), _stream()))

@@ -634,6 +634,133 @@ KVQ_API int kvq_paged_append_decode(const kvq_cfg* cfg, const void* const* plans
                                     kvq_stream_t stream);
 
 /*
+ * Page bookkeeping on the GPU (no counterpart in the pages): block tables and
+ * slot maps of a serving step from the requests' lengths, so that a step needs
+ * no host round trip and can be captured in a graph. The state is the caller's:
+ * block_table: device int32 [batch][max_pages], as in kvq_pages; entries past a
+ *              sequence's held pages are -1.
+ * held:        device int32 [batch], pages each sequence holds.
+ * free_ids:    device int32 [n_pages], a ring of free page ids; free_ring:
+ *              device int64 [2] = {index of the first free id, their number}.
+ * A fresh state has block_table = -1, held = 0, free_ids = every id once,
+ * free_ring = {0, n_pages}.
+ *
+ * kvq_pages_assign: afterwards sequence b holds exactly the pages of its first
+ *   len[b] + n_new[b] tokens, ceil((len + n_new) / (32 page_tiles)). Pages it
+ *   holds beyond that (a finished request with len = n_new = 0, a rolled-back
+ *   length) go to the tail of the ring first, in sequence, then row order; then
+ *   the missing pages are taken from its head in sequence order. Outputs, for
+ *   the step's new tokens as one packed batch (token j of sequence b is token
+ *   cu[b] + j): cu_dev int32 [batch + 1], the exclusive prefix sum of n_new;
+ *   slot_dev int64 [n_slots], the token's slot, page * 32 page_tiles + position
+ *   in the page; pos_dev int32 [n_slots] or NULL, its position in the sequence,
+ *   len[b] + j. Entries from cu[batch] on are left as they were.
+ *   A request that cannot be served is refused whole: its pages stay as they
+ *   are, its slots are -1, and the CAPACITY flag is set. That is: a negative
+ *   length or count, more tokens than its table row holds, tokens past n_slots,
+ *   or too few free pages (from the first such sequence on, no later sequence
+ *   gets pages either). held outside 0..max_pages refuses the sequence with
+ *   BAD_PAGE; a ring whose head or count is out of range, or that would
+ *   overflow, refuses the whole call with BAD_PAGE.
+ *   len_dev and n_new_dev (int32 [batch]) are only read; the append that fills
+ *   the slots advances the lengths. batch 1..65535, n_slots 0..2^31 - 1.
+ *   ws_dev: >= kvq_pages_assign_workspace_bytes(batch) bytes, 16-byte aligned,
+ *   contents overwritten; calls that overlap need workspaces of their own. The
+ *   result does not depend on timing.
+ */
+typedef struct kvq_page_state {
+  int32_t* block_table;
+  int32_t* held;
+  int32_t* free_ids;
+  int64_t* free_ring;
+  int64_t n_pages;
+  int32_t page_tiles;
+  int32_t max_pages;
+} kvq_page_state;
+
+KVQ_API size_t kvq_pages_assign_workspace_bytes(int batch); /* 0 if invalid */
+KVQ_API int kvq_pages_assign(const kvq_page_state* state, const int32_t* len_dev,
+                             const int32_t* n_new_dev, int batch, int64_t n_slots,
+                             int32_t* cu_dev, int64_t* slot_dev, int32_t* pos_dev, void* ws_dev,
+                             size_t ws_bytes, uint32_t* status_dev, kvq_stream_t stream);
+
+/*
+ * kvq_paged_quantize_append for a packed ragged batch (sequences of different
+ * lengths, no padding): row i of k_dev, v_dev ([n_rows][n_kv_heads][128] of type
+ * dtype) goes to slot slot_dev[i]; sequence b has rows cu_dev[b] .. cu_dev[b+1]-1,
+ * in order. cu_dev and slot_dev as kvq_pages_assign writes them for lengths
+ * len_dev; rows from cu[batch] on are not read. Codes, norms and the treatment of
+ * part-filled tiles are those of kvq_quantize_append. Then len_dev[b] += its rows.
+ * A sequence whose first slot is -1 was refused: nothing is stored, its length
+ * stays (a tile whose slot is -1 is skipped). A slot outside the pool, or slots
+ * of a tile that do not follow len, flag BAD_PAGE and skip the tile; cu outside
+ * 0..n_rows or a negative or overflowing length flags CAPACITY and skips the
+ * sequence. Different sequences' slots must not lie in one tile.
+ * pool, n_pages, page_tiles: as in kvq_pages. n_rows 0..2^31 - 1 (0: no work).
+ * rope_base = 0: post-RoPE keys; rope_base > 1: pre-RoPE keys, each rotated to
+ * its position as by kvq_quantize_append_rope. Two launches.
+ */
+KVQ_API int kvq_paged_append_ragged(const kvq_cfg* cfg, const void* const* plans_dev,
+                                    const void* k_dev, const void* v_dev, int dtype,
+                                    int64_t n_rows, const int32_t* cu_dev,
+                                    const int64_t* slot_dev, int batch, void* pool,
+                                    int64_t n_pages, int32_t page_tiles, int32_t* len_dev,
+                                    double rope_base, uint32_t* status_dev, kvq_stream_t stream);
+
+/*
+ * Decode attention for a batch whose sequences share long prefixes (no
+ * counterpart in the pages): sequence b, group_start[g] <= b < group_start[g+1],
+ * attends over the tokens of prefix g followed by its own,
+ *   o_h = sum_t softmax_t(q_h . k_hat_t / sqrt(128)) v_hat_t
+ * over both, k_hat and v_hat as for kvq_decode_attn. A prefix is unpacked once
+ * for up to 256 query rows (sequences x query heads of a KV head) on the tensor
+ * cores, so its cost does not grow with each sequence that shares it.
+ * prefix caches: n_prefixes caches (kvq_prefix_decode_attn) or block-table rows
+ *        (kvq_paged_prefix_decode_attn; same pool as the sequences or another),
+ *        prefix_len_dev int32 [n_prefixes], each <= max_prefix_len.
+ * group_start_dev: int32 [n_prefixes + 1], ascending in 0..batch (anything else
+ *        is clamped and flags BAD_PAGE). Groups may be empty; sequences before
+ *        the first group's start or from the last end on have no prefix.
+ * plans_dev: as for kvq_decode_attn. Prefix g was coded with the plans of its
+ *        group's first sequence; the plans of all its sequences must have that
+ *        plan's value signs (else BAD_PLAN), as the plans of one layer do.
+ * len_dev: int32 [batch], each sequence's own tokens, each <= max_len (0: only
+ *        the prefix). A sequence without any token gives 0. Lengths above their
+ *        bound are clamped and flag CAPACITY.
+ * q_dev: [batch][n_q_heads][128] of q_dtype (post-RoPE, at each sequence's full
+ *        position); out_dev: the same shape of out_dtype (KVQ_BF16, KVQ_FP16 or
+ *        KVQ_FP32), 16-byte aligned. For KVQ_BF16 the scaled query rows and the
+ *        attention weights enter the products rounded to fp16 (relative 2^-11
+ *        at most); for KVQ_FP16 and KVQ_FP32 as pairs of fp16 terms (about 22
+ *        bits), so an fp32 output is good to about 1e-6 of its norm.
+ * ws_dev: >= kvq_prefix_decode_workspace_bytes(...) bytes, 256-byte aligned;
+ *        contents overwritten, no initial value; calls that overlap on the GPU
+ *        need workspaces of their own.
+ * n_prefixes 1..1024. Three launches; results do not depend on timing (the same
+ * bits on every run). Other flags as for kvq_paged_decode_attn.
+ */
+KVQ_API size_t kvq_prefix_decode_workspace_bytes(const kvq_cfg* cfg, int batch, int n_q_heads,
+                                                 int n_prefixes);
+KVQ_API int kvq_prefix_decode_attn(const kvq_cfg* cfg, const void* const* plans_dev,
+                                   const void* const* prefix_cache_dev,
+                                   const int32_t* prefix_len_dev, const int32_t* group_start_dev,
+                                   int n_prefixes, int64_t max_prefix_len,
+                                   const void* const* cache_dev, const int32_t* len_dev,
+                                   int batch, int64_t max_len, const void* q_dev, int q_dtype,
+                                   int n_q_heads, void* out_dev, int out_dtype, void* ws_dev,
+                                   size_t ws_bytes, uint32_t* status_dev, kvq_stream_t stream);
+KVQ_API int kvq_paged_prefix_decode_attn(const kvq_cfg* cfg, const void* const* plans_dev,
+                                         const kvq_pages* prefix_pages,
+                                         const int32_t* prefix_len_dev,
+                                         const int32_t* group_start_dev, int n_prefixes,
+                                         int64_t max_prefix_len, const kvq_pages* pages,
+                                         const int32_t* len_dev, int batch, int64_t max_len,
+                                         const void* q_dev, int q_dtype, int n_q_heads,
+                                         void* out_dev, int out_dtype, void* ws_dev,
+                                         size_t ws_bytes, uint32_t* status_dev,
+                                         kvq_stream_t stream);
+
+/*
  * bf16 comparator (not part of the method): split-K decode attention over an
  * unquantized bf16 cache, built like kvq_decode_attn, to measure the packed
  * path against the dense one on the same shapes ("RoPE-Aware Bit Allocation
