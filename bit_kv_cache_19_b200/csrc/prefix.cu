@@ -26,7 +26,7 @@
 //     query rows) and (sequence, KV head); the units' 128-token tiles form one
 //     line of cost, cut evenly over the CTAs (a CTA takes a piece of one long
 //     unit or many short ones), so ragged lengths need no tuning. Warp roles:
-//     one warp streams 32-token records (bulk copies), six unpack codes into
+//     one warp walks the units, one streams 32-token records, 13 unpack codes into
 //     fp16 tiles in shared memory, one thread issues tcgen05.mma, two warpgroups
 //     run the softmax of two independent streams. A unit of more than 128 rows
 //     puts one 128-row tile in each stream (both use every K/V tile); a smaller
@@ -50,16 +50,16 @@ __device__ __align__(16) const uint32_t g_plut[KVQ_LUT_BYTES / 4] = KVQ_LUT_IMAG
 static_assert(KVQ_LUT_BYTES >= 512 * 16 + 128, "placeholder source of a refused page's tile");
 
 constexpr int kTok = 128;       // tokens of a K/V tile
-constexpr int kPThreads = 512;  // 2 softmax warpgroups, copy, MMA and 6 unpack warps
-constexpr int kUnpackWarps = 6;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kUnpackWarp0 = 10;
-constexpr int kDescUsers = 8 + 1 + kUnpackWarps;  // warps that read a segment descriptor
+constexpr int kPThreads = 768;  // 2 softmax warpgroups, 3 single warps, 13 unpack warps
+constexpr int kUnpackWarps = 13;
+constexpr int kWalkWarp = 8, kMmaWarp = 9, kCopyWarp = 10, kUnpackWarp0 = 11;
+constexpr int kDescUsers = 8 + 2 + kUnpackWarps;  // warps that read a segment descriptor
 constexpr uint32_t kPanel = 16384;                // 128 rows x 64 fp16, swizzled
 constexpr uint32_t kTileBytes = 2 * kPanel;
 constexpr uint32_t kQImage = 2 * kTileBytes;      // one unit's query image
 constexpr int kSufRows = 16;                      // rows of a sequence's query image
 constexpr uint32_t kSufImage = 2 * 2 * kSufRows * 128;  // 2 panels, hi and lo
-constexpr int kMaxRing = 8;
+constexpr int kMaxRing = 8;  // tiles in flight
 constexpr int kNormSlots = 4;
 // TMEM columns
 constexpr uint32_t kColS = 0, kColO = 256;
@@ -73,10 +73,11 @@ constexpr int kCostSeg = 3, kCostShared = 5, kCostAlt = 3;
 struct PfxHead {
   int64_t total;    // cost of all units
   int64_t suffix0;  // cost of the prefix units
-  int64_t n_punits;
+  int64_t n_cuts;   // CTAs that get a piece of the cost line
+  int64_t pad;
 };
 struct PfxLayout {
-  size_t head, gstart, gunit, gcost, scost, isc_p, isc_s, q_p, q_s, ml_p, ml_s, o_p, o_s, bytes;
+  size_t head, cuts, gstart, gunit, gcost, scost, isc_p, isc_s, q_p, q_s, ml_p, ml_s, o_p, o_s, bytes;
 };
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -96,6 +97,7 @@ static PfxLayout pfx_layout(int batch, int n_q, int n_kv, int n_groups, int n_ct
     return a;
   };
   w.head = take(sizeof(PfxHead));
+  w.cuts = take((size_t)(n_ctas + 1) * 8);
   w.gstart = take((size_t)(n_groups + 1) * 4);
   w.gunit = take((size_t)(n_groups + 1) * 4);
   w.gcost = take((size_t)(n_groups + 1) * 8);
@@ -117,13 +119,14 @@ struct PrefixParams {
   int G, tile_bytes, n_ctas;
   int rows_unit;  // 256 or 128 rows per prefix unit
   PfxHead* head;
+  int64_t* cuts;  // [n_ctas + 1] first position of each CTA's piece
   int32_t *gstart, *gunit;
   int64_t *gcost, *scost;
   float *isc_p, *isc_s;
   uint8_t *q_p, *q_s;
   float2 *ml_p, *ml_s;
   float *o_p, *o_s;
-  int ring, slot_bytes;
+  int ring;  // tile slots (4 records each)
 };
 
 __device__ __forceinline__ int clamp_len(int32_t l, int64_t most) {
@@ -151,14 +154,13 @@ __device__ __forceinline__ int64_t seq_cost(int tiles, int n_kv) {
   return tiles > 0 ? (int64_t)n_kv * (kCostSeg + (int64_t)tiles * kCostAlt) : 0;
 }
 
-// First position of CTA c's piece of the cost line.
-__device__ __forceinline__ int64_t cut(int64_t total, int c, int n) { return total * c / n; }
 // Number of a unit's tiles that start before position x of the cost line.
 __device__ __forceinline__ int tiles_before(int64_t x, int64_t start, int tiles, bool shared) {
   const int64_t d = x - start - kCostSeg;
   if (d <= 0) return 0;
-  const int64_t n = shared ? (d + kCostShared - 1) / kCostShared : (d + kCostAlt - 1) / kCostAlt;
-  return (int)min(n, (int64_t)tiles);
+  if (d >= (int64_t)tiles * (shared ? kCostShared : kCostAlt)) return tiles;
+  const uint32_t e = (uint32_t)d;  // tiles < 2^24
+  return (int)(shared ? (e + kCostShared - 1) / kCostShared : (e + kCostAlt - 1) / kCostAlt);
 }
 
 // ---------------------------------------------------------------------- prep
@@ -274,6 +276,10 @@ __device__ void prep_schedule(const PrefixParams& p, PrepSmem& sm) {
     if (i < p.a.batch) p.scost[i] = base + before;
     base += total;
   }
+  // no more pieces than tiles of the dearer kind; the CTAs past them get none
+  const int64_t pieces = min((int64_t)p.n_ctas, max((int64_t)1, base / kCostShared));
+  for (int i = tid; i <= p.n_ctas; i += kPrepThreads)
+    p.cuts[i] = i < pieces ? base * i / pieces : base;
   if (tid == 0) {
     p.gcost[n] = suffix0;
     p.gstart[n] = sm.gstart[n];
@@ -281,15 +287,16 @@ __device__ void prep_schedule(const PrefixParams& p, PrepSmem& sm) {
     p.scost[p.a.batch] = base;
     p.head->total = base;
     p.head->suffix0 = suffix0;
-    p.head->n_punits = sm.gunit[n];
+    p.head->n_cuts = pieces;
   }
   if (flags) atomicOr(p.a.status, flags);
 }
 
 // One query row (a warp) as fp16 operand row `row` of the image at img (panel
-// stride `panel`), its low part at img_lo; isc gets 2^-sigma.
+// stride `panel`), its low part `lo` bytes on; isc gets 2^-sigma.
+template <bool SPLIT>
 __device__ __forceinline__ void prep_row(const PrefixParams& p, const PrepSmem& sm, bool plan_ok,
-                                         float* buf, int b, int head, uint8_t* img, uint8_t* img_lo,
+                                         float* buf, int b, int head, uint8_t* img, uint32_t lo,
                                          uint32_t panel, int row, float* isc, int lane) {
   const Plan& pl = sm.plan;
 #pragma unroll
@@ -316,9 +323,12 @@ __device__ __forceinline__ void prep_row(const PrefixParams& p, const PrepSmem& 
   }
 #pragma unroll
   for (int m = 16; m; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-  const int sigma = (mx > 0.f && isfinite(mx)) ? 14 - ilogbf(mx) : 0;
-  const float sc = ldexpf(1.f, min(sigma, 127));
-  if (lane == 0) *isc = ldexpf(1.f, -min(sigma, 127));
+  // 2^sigma puts the row's largest element in [2^14, 2^15); 0 for a zero, inf
+  // or NaN row; at most 126, so that both powers are normal
+  const int ex = (int)(__float_as_uint(mx) >> 23);  // biased exponent
+  const int sigma = mx > 0.f && ex < 255 ? min(14 + 127 - ex, 126) : 0;
+  const float sc = __int_as_float((127 + sigma) << 23);
+  if (lane == 0) *isc = __int_as_float((127 - sigma) << 23);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float x0 = v[i].x * sc, x1 = v[i].y * sc;  // rank lane + 32 i
@@ -326,9 +336,9 @@ __device__ __forceinline__ void prep_row(const PrefixParams& p, const PrepSmem& 
     const uint32_t at = i * panel + row * 128 + ((((uint32_t)lane >> 2) ^ (row & 7)) << 4) +
                         (lane & 3) * 4;
     *reinterpret_cast<uint32_t*>(img + at) = hi;
-    if (img_lo) {
+    if constexpr (SPLIT) {
       const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
-      *reinterpret_cast<uint32_t*>(img_lo + at) =
+      *reinterpret_cast<uint32_t*>(img + lo + at) =
           pack_half2(x0 - __low2float(hh), x1 - __high2float(hh));
     }
   }
@@ -375,34 +385,41 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixP
     }
   }
   const bool grouped = g < n && sm.gstart[g] <= b;
-  const Plan* const own = p.a.plans[b] + h;
-  const Plan* const pre = grouped ? p.a.plans[sm.gstart[g]] + h : own;
-  bool ok = load_plan(p, sm, own);
-  uint8_t* const img = p.q_s + (size_t)bh * kSufImage;
-  for (int i = warp; i < p.G; i += kPrepThreads / 32)
-    prep_row(p, sm, ok, sm.row[warp], b, h * p.G + i, img,
-             SPLIT ? img + kSufImage / 2 : nullptr, kSufRows * 128, i,
-             p.isc_s + (size_t)b * p.a.n_q + h * p.G + i, lane);
-  if (!grouped) return;
-  if (pre != own) {
-    uint32_t sign[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sign[i] = sm.plan.v_sign[i];
-    ok = load_plan(p, sm, pre);
+  uint32_t sign[4] = {0u, 0u, 0u, 0u};
+  const Plan* held = nullptr;
+  bool ok = false;
+  // image 0: the sequence's own part; 1: the prefix part
+#pragma unroll 1
+  for (int part = 0; part < (grouped ? 2 : 1); ++part) {
+    const Plan* const src = p.a.plans[part ? sm.gstart[g] : b] + h;
+    if (src != held) {
+      ok = load_plan(p, sm, src);
+      held = src;
+    }
     // records of both parts are merged before the rotation is undone
     bool same = true;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) same &= sign[i] == sm.plan.v_sign[i];
+    for (int i = 0; i < 4; ++i) {
+      if (part) same &= sign[i] == sm.plan.v_sign[i];
+      sign[i] = sm.plan.v_sign[i];
+    }
     if (!same && tid == 0) atomicOr(p.a.status, KVQ_FLAG_BAD_PLAN);
-  }
-  const int rows = (sm.gstart[g + 1] - sm.gstart[g]) * p.G;
-  const int nrt = (rows + p.rows_unit - 1) / p.rows_unit;
-  for (int i = warp; i < p.G; i += kPrepThreads / 32) {
-    const int rr = (b - sm.gstart[g]) * p.G + i, rt = rr / p.rows_unit, r = rr % p.rows_unit;
-    uint8_t* const u = p.q_p + (size_t)(sm.gunit[g] + h * nrt + rt) * kQImage;
-    prep_row(p, sm, ok, sm.row[warp], b, h * p.G + i, SPLIT ? u : u + (r >> 7) * kTileBytes,
-             SPLIT ? u + kTileBytes : nullptr, kPanel, r & 127,
-             p.isc_p + (size_t)b * p.a.n_q + h * p.G + i, lane);
+    const int rows = (sm.gstart[g + 1] - sm.gstart[g]) * p.G;
+    const int nrt = (rows + p.rows_unit - 1) / p.rows_unit;
+#pragma unroll 1
+    for (int i = warp; i < p.G; i += kPrepThreads / 32) {
+      const int rr = (b - sm.gstart[g]) * p.G + i, rt = rr / p.rows_unit, r = rr % p.rows_unit;
+      uint8_t* img = p.q_s + (size_t)bh * kSufImage;
+      uint32_t lo = kSufImage / 2;
+      if (part) {
+        img = p.q_p + (size_t)(sm.gunit[g] + h * nrt + rt) * kQImage;
+        lo = kTileBytes;
+        if (!SPLIT) img += (r >> 7) * kTileBytes;
+      }
+      prep_row<SPLIT>(p, sm, ok, sm.row[warp], b, h * p.G + i, img, lo,
+                      part ? kPanel : kSufRows * 128, part ? r & 127 : i,
+                      (part ? p.isc_p : p.isc_s) + (size_t)b * p.a.n_q + h * p.G + i, lane);
+    }
   }
 }
 
@@ -412,6 +429,8 @@ struct alignas(16) Desc {  // one segment: a run of tiles of one unit
   float2* ml;
   float* o;
   const float* isc;
+  unsigned long long base[32];  // page bases of the first 32 records (0: refused)
+  int suffix, row, n_ranks;     // cache map and its row
   int stop, shared, rows, tiles, tile0, len, b0, row0, h, qslot, sub;
 };
 
@@ -420,14 +439,17 @@ struct alignas(128) MainSmem {
   Desc desc[2];
   alignas(16) float nk[kNormSlots][kTok];
   alignas(16) float nv[kNormSlots][kTok];
-  int lg[kNormSlots][4];  // per record: the value norms are below 2^lg
+  // per record: the value norms are below 2^lg; bounds of the key norms
+  alignas(16) int lg[kNormSlots][4];
+  alignas(16) float kmax[kNormSlots][4];
+  alignas(16) float kmin[kNormSlots][4];
   unsigned long long desc_full[2], desc_empty[2], ring_full[kMaxRing], ring_empty[kMaxRing];
-  unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full, v_empty;
   unsigned long long s_full[2], p_ready[2], o_full[2], o_free[2], lut_full, drain;
   uint32_t tmem;
   int fail;
 };
-constexpr size_t kMainTiles = 6 * (size_t)kTileBytes;  // Q x 2, K x 2, V x 2
+constexpr size_t kMainTiles = 5 * (size_t)kTileBytes;  // Q x 2, K x 2, V
 constexpr size_t kMaxSmem = 227 * 1024;
 static_assert(offsetof(MainSmem, desc) % 16 == 0 && sizeof(Desc) % 16 == 0, "bulk destinations");
 
@@ -435,9 +457,9 @@ static_assert(offsetof(MainSmem, desc) % 16 == 0 && sizeof(Desc) % 16 == 0, "bul
 // its loop, and the CTA drains and ends with the TIMEOUT flag.
 __device__ __forceinline__ bool wait_on(MainSmem& sm, unsigned long long* bar, uint32_t phase) {
   if (mbar_try_wait(bar, phase)) return true;
-  const long long t0 = clock64();
+  const uint32_t t0 = (uint32_t)clock();
   while (!mbar_try_wait(bar, phase)) {
-    if (clock64() - t0 > kWaitCycles || *(volatile int*)&sm.fail) {
+    if ((uint32_t)clock() - t0 > (uint32_t)kWaitCycles || *(volatile int*)&sm.fail) {
       *(volatile int*)&sm.fail = 1;
       return false;
     }
@@ -451,7 +473,18 @@ __device__ __forceinline__ bool wait_warp(MainSmem& sm, unsigned long long* bar,
   return __all_sync(0xffffffffu, wait_on(sm, bar, phase));
 }
 
-// Unit of work during the copy warp's walk along the cost line (warp-uniform).
+// Position in the ring of tile slots and its phase.
+struct RingPos {
+  uint32_t slot, phase;
+  __device__ __forceinline__ void next(uint32_t ring) {
+    if (++slot == ring) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Unit of work during the walk along the cost line (warp-uniform).
 struct Unit {
   bool suffix, shared;
   int g, b, h, rt;    // prefix: group, KV head, row tile; suffix: sequence, KV head
@@ -507,262 +540,265 @@ __device__ __forceinline__ int warp_last_le(const int64_t* a, int n, int64_t x, 
   return lo;
 }
 
+// The unit with cost at position x of the cost line.
 __device__ __forceinline__ Unit unit_at(const PrefixParams& p, int64_t x, int64_t suffix0,
                                         int lane) {
-  if (x < suffix0) {
-    const int g = warp_last_le(p.gcost, p.a.n_groups, x, lane);
-    const int rows = (p.gstart[g + 1] - p.gstart[g]) * p.G;
-    const GroupCost c =
-        group_cost(rows, tiles_of(clamp_len(p.a.pre_len[g], p.a.max_pre)), p.rows_unit);
-    const int64_t d = x - p.gcost[g];
-    const int h = (int)(d / c.block);
-    const int rt = (int)min((d - h * c.block) / c.full, (int64_t)c.nrt - 1);
-    return prefix_unit(p, g, h, rt);
+  const bool suffix = x >= suffix0;
+  const int i = warp_last_le(suffix ? p.scost : p.gcost, suffix ? p.a.batch : p.a.n_groups, x, lane);
+  if (suffix) {
+    Unit u = suffix_unit(p, i, 0);
+    while (u.start + u.cost <= x && u.h + 1 < p.a.n_kv) {
+      ++u.h;
+      u.start += u.cost;
+      ++u.idx;
+    }
+    return u;
   }
-  const int b = warp_last_le(p.scost, p.a.batch, x, lane);
-  const Unit u = suffix_unit(p, b, 0);
-  return u.cost > 0 ? suffix_unit(p, b, (int)min((x - u.start) / u.cost, (int64_t)p.a.n_kv - 1))
-                    : u;
+  const int rows = (p.gstart[i + 1] - p.gstart[i]) * p.G;
+  const GroupCost c =
+      group_cost(rows, tiles_of(clamp_len(p.a.pre_len[i], p.a.max_pre)), p.rows_unit);
+  int64_t d = x - p.gcost[i];
+  int h = 0;
+  for (; d >= c.block && h + 1 < p.a.n_kv; ++h) d -= c.block;
+  const int rt = (int)min(d / c.full, (int64_t)c.nrt - 1);
+  return prefix_unit(p, i, h, rt);
 }
 
-// 32 tokens of keys: one half step (<= 4 blocks of width W) of one record into
-// rows 32 rec + (0..31) of the K tile. Lane (g, c): block c, tokens g + 8 i.
-__device__ __forceinline__ void unpack_keys(const MainSmem& sm, const Plan& pl, const uint8_t* kw,
-                                            int hs, uint8_t* tile, int rec, int lane) {
+// What a lane needs to unpack one half step (<= 4 blocks of width W) of a
+// record: lane (g, c) = (lane / 4, lane mod 4) takes block c, tokens g + 8 i,
+// i < 4, whose four 2W-bit fields are contiguous.
+struct KeyStep {
+  uint32_t src;   // byte offset of its first word in the record's key words
+  uint32_t shw;   // first bit in that word | W << 8
+  uint32_t dst;   // byte offset of token g's pair in the K tile, bit 31: no block
+};
+__device__ __forceinline__ KeyStep key_step(const Plan& pl, int hs, int lane) {
   const int g = lane >> 2, c = lane & 3;
-  const int W = pl.hs_width[hs], r0 = pl.hs_rank0[hs], n = pl.hs_count[hs];
-  const int cc = min(c, n - 1), rank = r0 + cc;
-  const int off = pl.seg_off[r0] + 2 * W * cc + ((W * g) >> 2);
-  const uint32_t sh = (uint32_t)(8 * W * g) & 31u;
-  const uint8_t* wp = kw + 4 * off;
-  const uint8_t* lut = sm.lut;
-  const uint32_t w2 = 2u * (uint32_t)W;
-  uint32_t A[4];
-  if (W <= 3) {
-    const uint32_t m7 = ((1u << w2) - 1u) << 7;
-    const uint32_t lb = ((uint32_t)lane * 4u) | (W == 1 ? 0x4000u : W == 2 ? 0x2000u : 0u);
-    const uint32_t v7 = funnel_r(*reinterpret_cast<const uint32_t*>(wp),
-                                 *reinterpret_cast<const uint32_t*>(wp + 4), sh) << 7;
+  const int W = pl.hs_width[hs], r0 = pl.hs_rank0[hs], nb = pl.hs_count[hs];
+  const int cc = min(c, nb - 1), rank = r0 + cc;
+  KeyStep k;
+  k.src = 4u * (uint32_t)(pl.seg_off[r0] + 2 * W * cc + ((W * g) >> 2));
+  k.shw = ((uint32_t)(8 * W * g) & 31u) | (uint32_t)W << 8;
+  k.dst = (uint32_t)(rank >> 5) * kPanel + (uint32_t)g * 128u +
+          ((((uint32_t)rank & 31u) >> 2 ^ (uint32_t)g) << 4) + (uint32_t)(rank & 3) * 4u;
+  if (c >= nb) k.dst |= 0x80000000u;
+  return k;
+}
+
+// One half step of the four records whose key words are at w, into the K tile
+// at dst (32 rows each). The records are independent lookup chains, which hides their latency; a tile's missing
+// records repeat earlier ones (their positions are masked in the softmax).
+__device__ __forceinline__ void unpack_keys(const KeyStep& k, const uint8_t* lut,
+                                            const uint8_t* const (&w)[4], uint8_t* dst, int lane) {
+  const uint32_t sh = k.shw & 31u, W = k.shw >> 8, w2 = 2u * W, mask = (1u << w2) - 1u;
+  const bool store = !(k.dst >> 31);
+  uint8_t* const to = dst + (k.dst & 0x7FFFFFFFu);
+  if (W <= 3) {  // pair table replicated per lane, at most 24 bits
+    const uint32_t lb = (uint32_t)lane * 4u | (W == 1 ? 0x4000u : W == 2 ? 0x2000u : 0u);
+    const uint32_t m7 = mask << 7;
+    uint32_t v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      A[i] = *reinterpret_cast<const uint32_t*>(lut + (((v7 >> (w2 * i)) & m7) | lb));
-  } else {
-    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wp);
-    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wp + 4);
-    const uint32_t x2 = W > 4 ? *reinterpret_cast<const uint32_t*>(wp + 8) : 0u;
-    const unsigned long long v = ((unsigned long long)funnel_r(w1, x2, sh) << 32) |
-                                 funnel_r(w0, w1, sh);
-    if (W <= 5) {  // pair tables
-      const uint8_t* tab = lut + (W == 4 ? 0x2800u : 0x2C00u);
-      const uint32_t m = (1u << w2) - 1u;
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t* a = reinterpret_cast<const uint32_t*>(w[r] + k.src);
+      v[r] = funnel_r(a[0], a[1], sh) << 7;
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        A[i] = *reinterpret_cast<const uint32_t*>(tab + 4u * ((uint32_t)(v >> (w2 * i)) & m));
-    } else {  // single codes
-      const uint8_t* tab = lut + 0x3C00u + 2u * (uint32_t)((1 << W) - 2);
-      const uint32_t m = (1u << W) - 1u;
+    for (int i = 0; i < 4; ++i) {
+      uint32_t x[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = *reinterpret_cast<const uint32_t*>(lut + ((v[r] & m7) | lb));
+        v[r] >>= w2;
+      }
+      if (store) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<uint32_t*>(to + r * 4096 + i * 1024) = x[r];
+      }
+      // v keeps its code bits 7 places up, so the shift must not pull bits in
+      // from below bit 7: they are masked by m7
+    }
+    return;
+  }
+  // widths 4, 5: one pair table; wider: two single-code lookups
+  const uint8_t* tab = lut + (W == 4 ? 0x2800u : W == 5 ? 0x2C00u
+                                                        : 0x3C00u + 2u * (uint32_t)((1 << W) - 2));
+#pragma unroll 1
+  for (int r = 0; r < 4; r += 2) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint8_t* src = r ? w[2 + q] : w[q];
+      const uint32_t* a = reinterpret_cast<const uint32_t*>(src + k.src);
+      const uint32_t a1 = a[1], hi = W > 4 ? funnel_r(a1, a[2], sh) : 0u;
+      const unsigned long long v = ((unsigned long long)hi << 32) | funnel_r(a[0], a1, sh);
+      uint32_t x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t f = (uint32_t)(v >> (w2 * i));
-        A[i] = *reinterpret_cast<const uint16_t*>(tab + 2u * (f & m)) |
-               ((uint32_t)*reinterpret_cast<const uint16_t*>(tab + 2u * ((f >> W) & m)) << 16);
+        if (W <= 5)
+          x[i] = *reinterpret_cast<const uint32_t*>(tab + 4u * (f & mask));
+        else
+          x[i] = *reinterpret_cast<const uint16_t*>(tab + 2u * (f & (mask >> W))) |
+                 ((uint32_t)*reinterpret_cast<const uint16_t*>(
+                      tab + 2u * ((f >> W) & (mask >> W))) << 16);
+      }
+      if (store) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint32_t*>(to + (r + q) * 4096 + i * 1024) = x[i];
       }
     }
-  }
-  if (c < n) {
-    uint8_t* dst = tile + (rank >> 5) * kPanel + (32 * rec + g) * 128 +
-                   ((((uint32_t)rank & 31u) >> 2 ^ (uint32_t)g) << 4) + (rank & 3) * 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(dst + i * 8 * 128) = A[i];
   }
 }
 
-// 8 rotated value coordinates (rows 8 m .. 8 m + 7 of the V tile) of the 32
-// tokens of record `rec`. Lane (g, c): coordinate 8 m + g, tokens 8 i + 2 c + (0, 1).
+// The BV words of one rotated coordinate of a record (32 tokens).
 template <int BV>
-__device__ __forceinline__ void unpack_values(const MainSmem& sm, const uint8_t* vw, int m,
-                                              uint8_t* tile, int rec, int lane) {
-  const int g = lane >> 2, c = lane & 3, row = 8 * m + g;
-  const uint8_t* wp = vw + 4 * (row * BV + ((BV * c) >> 2));
-  const uint32_t sh = (uint32_t)(8 * BV * c) & 31u;
-  const uint8_t* lut = sm.lut;
-  uint32_t F[4];
-  if constexpr (BV <= 3) {
-    constexpr uint32_t m7 = ((1u << (2 * BV)) - 1u) << 7;
-    const uint32_t lb = ((uint32_t)lane * 4u) | (BV == 1 ? 0x4000u : BV == 2 ? 0x2000u : 0u);
-    const uint32_t v7 = funnel_r(*reinterpret_cast<const uint32_t*>(wp),
-                                 *reinterpret_cast<const uint32_t*>(wp + 4), sh) << 7;
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[BV + 1]) {
+  if constexpr (BV % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      F[i] = *reinterpret_cast<const uint32_t*>(lut + (((v7 >> (2 * BV * i)) & m7) | lb));
+    for (int i = 0; i < BV / 4; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
+    }
+  } else if constexpr (BV % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < BV / 2; ++i) {
+      const uint2 x = reinterpret_cast<const uint2*>(p)[i];
+      w[2 * i] = x.x;
+      w[2 * i + 1] = x.y;
+    }
   } else {
-    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wp);
-    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wp + 4);
-    const uint32_t x2 = BV > 4 ? *reinterpret_cast<const uint32_t*>(wp + 8) : 0u;
-    const unsigned long long v = ((unsigned long long)funnel_r(w1, x2, sh) << 32) |
-                                 funnel_r(w0, w1, sh);
-    if constexpr (BV <= 5) {
-      const uint8_t* tab = lut + (BV == 4 ? 0x2800u : 0x2C00u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        F[i] = *reinterpret_cast<const uint32_t*>(
-            tab + 4u * ((uint32_t)(v >> (2 * BV * i)) & ((1u << (2 * BV)) - 1u)));
-    } else {
-      const uint8_t* tab = lut + 0x3C00u + 2u * (uint32_t)((1 << BV) - 2);
-      constexpr uint32_t mm = (1u << BV) - 1u;
+    for (int i = 0; i < BV; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+  w[BV] = 0u;
+}
+
+// 32 tokens of one rotated value coordinate (a lane's row of the V tile) as
+// fp16: the pair of tokens 8 i + 2 c + (0, 1) sits at bit (8 c + 2 i) BV, so
+// the 16-byte chunk of tokens 8 i .. 8 i + 7 takes its four pairs from the
+// four quarters of the words. Chunk i goes to dst + ((chunk0 + i) ^ sw) * 16.
+template <int BV>
+__device__ __forceinline__ void unpack_values(const uint8_t* lut, const uint8_t* src,
+                                              uint32_t lane4, uint8_t* dst, uint32_t chunk0,
+                                              uint32_t sw) {
+  uint32_t w[BV + 1];
+  load_words<BV>(src, w);
+  constexpr uint32_t mask = (1u << (2 * BV)) - 1u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t f = (uint32_t)(v >> (2 * BV * i));
-        F[i] = *reinterpret_cast<const uint16_t*>(tab + 2u * (f & mm)) |
-               ((uint32_t)*reinterpret_cast<const uint16_t*>(tab + 2u * ((f >> BV) & mm)) << 16);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int o = (8 * c + 2 * i) * BV, k = o >> 5, s = o & 31;
+      const bool spill = s + 2 * BV > 32;
+      if constexpr (BV <= 3) {  // table entries are 128 bytes apart, one copy per lane
+        const uint32_t lb = lane4 | (BV == 1 ? 0x4000u : BV == 2 ? 0x2000u : 0u);
+        const uint32_t v = spill ? funnel_r(w[k], w[k + 1], (s - 7) & 31)
+                           : s >= 7 ? w[k] >> ((s - 7) & 31) : w[k] << ((7 - s) & 31);
+        x[c] = *reinterpret_cast<const uint32_t*>(lut + ((v & (mask << 7)) | lb));
+      } else {
+        const uint32_t v = spill ? funnel_r(w[k], w[k + 1], s) : w[k] >> s;
+        if constexpr (BV <= 5) {
+          x[c] = *reinterpret_cast<const uint32_t*>(lut + (BV == 4 ? 0x2800u : 0x2C00u) +
+                                                    4u * (v & mask));
+        } else {
+          const uint8_t* tab = lut + 0x3C00u + 2u * (uint32_t)((1 << BV) - 2);
+          constexpr uint32_t m1 = (1u << BV) - 1u;
+          x[c] = *reinterpret_cast<const uint16_t*>(tab + 2u * (v & m1)) |
+                 ((uint32_t)*reinterpret_cast<const uint16_t*>(tab + 2u * ((v >> BV) & m1)) << 16);
+        }
       }
     }
+    *reinterpret_cast<uint4*>(dst + (((chunk0 + i) ^ sw) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
   }
-  uint8_t* dst = tile + (rec >> 1) * kPanel + row * 128 + c * 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint32_t*>(dst + (((uint32_t)(4 * (rec & 1) + i) ^ (uint32_t)g) << 4)) = F[i];
 }
 
 // ---- the roles of the main kernel
 
+// Walks the CTA's piece of the cost line: one descriptor, plan and query image
+// per segment, ahead of the other roles.
 template <bool SPLIT>
-__device__ void copy_role(const PrefixParams& p, MainSmem& sm, uint8_t* qbuf, uint8_t* ring,
-                          int lane) {
-  const int64_t total = p.head->total, suffix0 = p.head->suffix0;
-  const int64_t x0 = cut(total, blockIdx.x, p.n_ctas), x1 = cut(total, blockIdx.x + 1, p.n_ctas);
-  const int bk = p.a.bits_k, bv = p.a.bits_v;
-  uint32_t seg = 0, rc = 0;        // segments, ring slots issued
+__device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, uint8_t* qbuf,
+                                          int lane) {
+  const int64_t suffix0 = p.head->suffix0;
+  const int64_t x0 = p.cuts[blockIdx.x], x1 = p.cuts[blockIdx.x + 1];
+  uint32_t seg = 0;                // segments
   uint32_t quse[2] = {0u, 0u};     // segments that used each query slot
   int qnext = 0;
   bool ok = true;
-  if (x0 < x1) {
-    Unit u = unit_at(p, x0, suffix0, lane);
-    while (ok && u.start < x1) {
-      const int t0 = tiles_before(x0, u.start, u.tiles, u.shared);
-      const int t1 = tiles_before(x1, u.start, u.tiles, u.shared);
-      if (t0 < t1) {
-        // ---- descriptor, plan and query rows
-        const uint32_t ds = seg & 1;
-        if (!wait_warp(sm, &sm.desc_empty[ds], ((seg >> 1) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        const bool both = u.shared || SPLIT;
-        const int qs = both ? 0 : qnext;
-        if (lane == 0) {
-          Desc& d = sm.desc[ds];
-          const size_t inc = (size_t)blockIdx.x + (size_t)u.idx;
-          d.ml = u.suffix ? p.ml_s + inc * 2 * p.G : p.ml_p + inc * 256;
-          d.o = u.suffix ? p.o_s + inc * 2 * p.G * kHeadDim : p.o_p + inc * 256 * kHeadDim;
-          d.isc = u.suffix ? p.isc_s : p.isc_p;
-          d.stop = 0;
-          d.shared = u.shared;
-          d.rows = u.rows;
-          d.tiles = t1 - t0;
-          d.tile0 = t0;
-          d.len = u.len;
-          d.b0 = u.b;
-          d.row0 = u.rt * p.rows_unit;
-          d.h = u.h;
-          d.qslot = qs;
-          d.sub = u.suffix ? p.G : 128;
-          mbar_expect_tx(&sm.desc_full[ds], KVQ_PLAN_BYTES);
-          bulk_g2s(&d.plan, p.a.plans[u.b] + u.h, KVQ_PLAN_BYTES, &sm.desc_full[ds]);
-        }
-        __syncwarp();
-        ++seg;
-        for (int i = 0; i < (both ? 2 : 1) && ok; ++i) {
-          const int s = qs + i;
-          ok = wait_warp(sm, &sm.q_empty[s], (quse[s] & 1) ^ 1);
-          if (!ok) break;
-          // rows of this slot: the row tile of stream i, or all rows (hi, lo)
-          const int rows = u.shared ? min(128, u.rows - 128 * i) : u.rows;
-          const uint32_t bytes = (uint32_t)(rows + 7) / 8 * 1024;
-          if (lane == 0) {
-            const uint8_t* src = u.suffix ? p.q_s + (size_t)u.idx * kSufImage + i * (kSufImage / 2)
-                                          : p.q_p + (size_t)u.idx * kQImage + i * kTileBytes;
-            const uint32_t panel = u.suffix ? kSufRows * 128 : kPanel;
-            mbar_expect_tx(&sm.q_full[s], 2 * bytes);
-            bulk_g2s(qbuf + s * kTileBytes, src, bytes, &sm.q_full[s]);
-            bulk_g2s(qbuf + s * kTileBytes + kPanel, src + panel, bytes, &sm.q_full[s]);
-          }
-          __syncwarp();
-          ++quse[s];
-        }
-        if (!both) qnext ^= 1;
-        // ---- packed records, keys then values of each tile; the pages of the
-        //      next 32 records are looked up by the 32 lanes at once
-        const CacheMap& cm = u.suffix ? p.a.own : p.a.pre;
-        const int row = u.suffix ? u.b : u.g;
-        const int n_rec = (u.len + kTile - 1) / kTile, mask = page_mask(cm);
-        unsigned long long base = 0;
-        for (int t = t0; t < t1 && ok; ++t) {
-          if (((t - t0) & 7) == 0) {
-            const int rec = 4 * t + lane;
-            base = rec < n_rec
-                       ? (unsigned long long)(uintptr_t)page_base(cm, row, rec) : 0ull;
-          }
-          for (int part = 0; part < 2 && ok; ++part)
-            for (int r = 0; r < 4; ++r) {
-              const int rec = 4 * t + r;
-              const unsigned long long pb =
-                  __shfl_sync(0xffffffffu, base, 4 * ((t - t0) & 7) + r);
-              if (rec >= n_rec) break;
-              const uint32_t slot = rc % p.ring;
-              ok = wait_warp(sm, &sm.ring_empty[slot], ((rc / p.ring) & 1) ^ 1);
-              if (!ok) break;
-              if (lane == 0) {
-                const uint8_t* src = reinterpret_cast<const uint8_t*>(g_plut);
-                if (pb && !(pb & 15))
-                  src = reinterpret_cast<const uint8_t*>((uintptr_t)pb) +
-                        ((size_t)(rec & mask) * p.a.n_kv + u.h) * p.tile_bytes;
-                else  // refused: placeholder bytes are streamed, the output is flagged
-                  atomicOr(p.a.status, pb ? KVQ_FLAG_BAD_PLAN : KVQ_FLAG_BAD_PAGE);
-                uint8_t* dst = ring + (size_t)slot * p.slot_bytes;
-                if (part == 0) {
-                  mbar_expect_tx(&sm.ring_full[slot], 512 * bk + 128);
-                  bulk_g2s(dst, src, 512 * bk, &sm.ring_full[slot]);
-                  bulk_g2s(dst + 512 * bk, src + 512 * (bk + bv), 128, &sm.ring_full[slot]);
-                } else {
-                  mbar_expect_tx(&sm.ring_full[slot], 512 * bv);
-                  bulk_g2s(dst, src + 512 * bk, 512 * bv, &sm.ring_full[slot]);
-                }
-              }
-              __syncwarp();
-              ++rc;
-            }
-        }
-      }
-      // ---- next unit with any cost
-      if (!u.suffix) {
-        int g = u.g, h = u.h, rt = u.rt + 1;
-        if (rt == u.nrt) {
-          rt = 0;
-          if (++h == p.a.n_kv) {
-            h = 0;
-            ++g;
-            while (g < p.a.n_groups && p.gcost[g + 1] == p.gcost[g]) ++g;
-          }
-        }
-        if (g < p.a.n_groups) {
-          u = prefix_unit(p, g, h, rt);
-          continue;
-        }
-        if (suffix0 >= x1) break;
-        u = unit_at(p, suffix0, suffix0, lane);
-        if (u.cost == 0) break;
-        continue;
-      }
-      int b = u.b, h = u.h + 1;
-      if (h == p.a.n_kv) {
-        h = 0;
-        const int64_t end = p.scost[b + 1];
-        if (end >= x1) break;
-        b = warp_last_le(p.scost, p.a.batch, end, lane);
-      }
-      u = suffix_unit(p, b, h);
+  int64_t x = x0;
+#pragma unroll 1
+  while (ok && x < x1) {
+    const Unit u = unit_at(p, x, suffix0, lane);
+    x = u.start + u.cost;
+    const int t0 = tiles_before(x0, u.start, u.tiles, u.shared);
+    const int t1 = tiles_before(x1, u.start, u.tiles, u.shared);
+    if (u.cost == 0) break;
+    if (t0 >= t1) continue;
+    const int row = u.suffix ? u.b : u.g, n_rec = (u.len + kTile - 1) / kTile;
+    const Plan* const plan = p.a.plans[u.b] + u.h;
+    const int n_ranks = plan->n_ranks;
+    unsigned long long base = 0;
+    if (4 * t0 + lane < n_rec)
+      base = (unsigned long long)(uintptr_t)page_base(u.suffix ? p.a.own : p.a.pre, row,
+                                                      4 * t0 + lane);
+    const uint32_t ds = seg & 1;
+    ok = wait_warp(sm, &sm.desc_empty[ds], ((seg >> 1) & 1) ^ 1);
+    if (!ok) break;
+    const bool both = u.shared || SPLIT;
+    const int qs = both ? 0 : qnext;
+    Desc& d = sm.desc[ds];
+    d.base[lane] = base;
+    __syncwarp();
+    if (lane == 0) {
+      const size_t inc = (size_t)blockIdx.x + (size_t)u.idx;
+      d.ml = u.suffix ? p.ml_s + inc * 2 * p.G : p.ml_p + inc * 256;
+      d.o = u.suffix ? p.o_s + inc * 2 * p.G * kHeadDim : p.o_p + inc * 256 * kHeadDim;
+      d.isc = u.suffix ? p.isc_s : p.isc_p;
+      d.suffix = u.suffix;
+      d.row = row;
+      d.n_ranks = n_ranks;
+      d.stop = 0;
+      d.shared = u.shared;
+      d.rows = u.rows;
+      d.tiles = t1 - t0;
+      d.tile0 = t0;
+      d.len = u.len;
+      d.b0 = u.b;
+      d.row0 = u.rt * p.rows_unit;
+      d.h = u.h;
+      d.qslot = qs;
+      d.sub = u.suffix ? p.G : 128;
+      mbar_expect_tx(&sm.desc_full[ds], KVQ_PLAN_BYTES);
+      bulk_g2s(&d.plan, plan, KVQ_PLAN_BYTES, &sm.desc_full[ds]);
     }
+    __syncwarp();
+    ++seg;
+#pragma unroll 1
+    for (int i = 0; i < (both ? 2 : 1); ++i) {
+      const int s = qs + i;
+      ok = wait_warp(sm, &sm.q_empty[s], (quse[0] * (s == 0) + quse[1] * (s == 1)) & 1 ^ 1);
+      if (!ok) break;
+      // rows of this slot: the row tile of stream i, or all rows (hi, lo)
+      const int rows = u.shared ? min(128, u.rows - 128 * i) : u.rows;
+      const uint32_t bytes = (uint32_t)(rows + 7) / 8 * 1024;
+      if (lane == 0) {
+        const uint8_t* src = u.suffix ? p.q_s + (size_t)u.idx * kSufImage + i * (kSufImage / 2)
+                                      : p.q_p + (size_t)u.idx * kQImage + i * kTileBytes;
+        const uint32_t panel = u.suffix ? kSufRows * 128 : kPanel;
+        mbar_expect_tx(&sm.q_full[s], 2 * bytes);
+        bulk_g2s(qbuf + s * kTileBytes, src, bytes, &sm.q_full[s]);
+        bulk_g2s(qbuf + s * kTileBytes + kPanel, src + panel, bytes, &sm.q_full[s]);
+      }
+      __syncwarp();
+      quse[0] += s == 0;
+      quse[1] += s == 1;
+    }
+    if (!both) qnext ^= 1;
   }
   if (ok) {  // the end of the CTA's work
     const uint32_t ds = seg & 1;
@@ -773,19 +809,87 @@ __device__ void copy_role(const PrefixParams& p, MainSmem& sm, uint8_t* qbuf, ui
     }
   }
   if (!ok) {  // let the copies in flight land before the CTA ends
-    for (uint32_t i = 0; i < (uint32_t)p.ring && i < rc; ++i)
-      (void)mbar_wait_bounded(&sm.ring_full[(rc - 1 - i) % p.ring], ((rc - 1 - i) / p.ring) & 1);
-    for (int s = 0; s < 2; ++s)
-      if (quse[s]) (void)mbar_wait_bounded(&sm.q_full[s], (quse[s] - 1) & 1);
+    if (quse[0]) (void)mbar_wait_bounded(&sm.q_full[0], (quse[0] - 1) & 1);
+    if (quse[1]) (void)mbar_wait_bounded(&sm.q_full[1], (quse[1] - 1) & 1);
     for (uint32_t i = 1; i <= 2 && i <= seg; ++i)
       (void)mbar_wait_bounded(&sm.desc_full[(seg - i) & 1], ((seg - i) >> 1) & 1);
   }
 }
 
+// Streams the segments' records into the ring, a tile (up to four records, one
+// bulk copy each) per slot.
+__device__ __forceinline__ void copy_role(const PrefixParams& p, MainSmem& sm, uint8_t* ring,
+                                          int lane) {
+  const uint32_t n_ring = p.ring, tbytes = p.tile_bytes;
+  RingPos rp{0u, 0u};
+  uint32_t issued = 0;  // slots that copies have been issued to
+  bool ok = true;
+  for (uint32_t seg = 0; ok; ++seg) {
+    const uint32_t ds = seg & 1;
+    ok = wait_warp(sm, &sm.desc_full[ds], (seg >> 1) & 1);
+    const Desc& d = sm.desc[ds];
+    if (!ok || d.stop) break;
+    const int tiles = d.tiles, n_rec = (d.len + kTile - 1) / kTile, row = d.row, h = d.h;
+    const int rec0 = 4 * d.tile0;
+    const bool suffix = d.suffix;
+    const int mask = suffix ? page_mask(p.a.own) : page_mask(p.a.pre);
+    const size_t rec_step = (size_t)p.a.n_kv * tbytes;
+    // lane: the source of record lane of each run of 32 (8 tiles); the pages of
+    // the next run are looked up a run ahead
+    auto page_of = [&](int rec) -> unsigned long long {
+      return rec < n_rec ? (unsigned long long)(uintptr_t)page_base(
+                               suffix ? p.a.own : p.a.pre, row, rec) : 0ull;
+    };
+    auto source = [&](unsigned long long base, int rec) -> unsigned long long {
+      if (rec >= n_rec) return 0ull;
+      if (base && !(base & 15)) return base + (size_t)(rec & mask) * rec_step + (size_t)h * tbytes;
+      // refused: placeholder bytes are streamed, the output is flagged
+      atomicOr(p.a.status, base ? KVQ_FLAG_BAD_PLAN : KVQ_FLAG_BAD_PAGE);
+      return (unsigned long long)(uintptr_t)g_plut;
+    };
+    unsigned long long src = source(d.base[lane], rec0 + lane), next = 0;
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t) {
+      if ((t & 7) == 0) {
+        if (t) src = source(next, rec0 + 4 * t + lane);
+        next = t + 8 < tiles ? page_of(rec0 + 4 * (t + 8) + lane) : 0ull;
+      }
+      const int n = min(4, n_rec - rec0 - 4 * t);
+      ok = wait_warp(sm, &sm.ring_empty[rp.slot], rp.phase ^ 1);
+      if (!ok) break;
+      uint8_t* const dst = ring + rp.slot * 4 * tbytes;
+      if (lane == 0) mbar_expect_tx(&sm.ring_full[rp.slot], (uint32_t)n * tbytes);
+      __syncwarp();
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const unsigned long long a = __shfl_sync(0xffffffffu, src, (4 * (t & 7) + i) & 31);
+        if (lane == 0)
+          bulk_g2s(dst + i * tbytes, reinterpret_cast<const void*>((uintptr_t)a), tbytes,
+                   &sm.ring_full[rp.slot]);
+      }
+      rp.next(n_ring);
+      issued = min(issued + 1, n_ring);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.desc_empty[ds]);
+  }
+  if (!ok)  // let the copies in flight land before the CTA ends: the last use of
+            // each slot had the ring's phase, or the one before
+    for (uint32_t i = 0; i < issued; ++i)
+      (void)mbar_wait_bounded(&sm.ring_full[i], i < rp.slot ? rp.phase : rp.phase ^ 1);
+}
+
 template <int BV>
-__device__ void unpack_role(const PrefixParams& p, MainSmem& sm, uint8_t* kbuf, uint8_t* vbuf,
+__device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm, uint8_t* kbuf, uint8_t* vbuf,
                             const uint8_t* ring, int uw, int lane) {
-  uint32_t seg = 0, rc = 0, tile_no = 0;
+  uint32_t seg = 0, tile_no = 0;
+  const uint32_t n_ring = p.ring;
+  RingPos rk{0u, 0u}, rv{0u, 0u};  // slots of the keys and of the values
+  // values lag a tile behind the keys where the ring holds two tiles: V of a tile
+  // is unpacked while its softmax runs, when the product before has freed the
+  // V tile
+  const int lag = n_ring > 1 ? 1 : 0;
+  const uint32_t tbytes = p.tile_bytes;
   if (!wait_warp(sm, &sm.lut_full, 0)) return;
   for (;; ++seg) {
     const uint32_t ds = seg & 1;
@@ -797,57 +901,71 @@ __device__ void unpack_role(const PrefixParams& p, MainSmem& sm, uint8_t* kbuf, 
                          pl.bits_v == BV && plan_sched_ok(pl, lane);
     if (!plan_ok && uw == 0 && lane == 0) atomicOr(p.a.status, KVQ_FLAG_BAD_PLAN);
     const int n_half = plan_ok ? pl.n_half : 0;
-    const int n_rec = (d.len + kTile - 1) / kTile, norm_off = 512 * p.a.bits_k;
+    const KeyStep k0 = key_step(pl, uw < n_half ? uw : 0, lane);
+    const KeyStep k1 = key_step(pl, uw + kUnpackWarps < n_half ? uw + kUnpackWarps : 0, lane);
+    const int n_steps = (uw < n_half) + (uw + kUnpackWarps < n_half);
+    const int n_rec = (d.len + kTile - 1) / kTile, key_bytes = 512 * p.a.bits_k;
+    const int norm_off = key_bytes + 512 * BV;
+    const int me = uw >= kUnpackWarps - 4 ? uw - (kUnpackWarps - 4) : 4;  // a record's norms, or none
     const int tiles = d.tiles, tile0 = d.tile0, len = d.len;
-    for (int t = 0; t < tiles; ++t, ++tile_no) {
-      const uint32_t st = tile_no & 1, ph = (tile_no >> 1) & 1, ns = tile_no % kNormSlots;
-      if (!wait_warp(sm, &sm.k_empty[st], ph ^ 1)) return;
-      for (int r = 0; r < 4; ++r) {
-        const int rec = 4 * (tile0 + t) + r;
-        if (rec < n_rec) {
-          const uint32_t slot = rc % p.ring;
-          if (!wait_warp(sm, &sm.ring_full[slot], (rc / p.ring) & 1)) return;
-          const uint8_t* w = ring + (size_t)slot * p.slot_bytes;
-          if (uw == r) {  // norms: masked tokens 0; an exponent above the value norms
-            const __half* nrm = reinterpret_cast<const __half*>(w + norm_off);
-            const bool in = rec * kTile + lane < len;
-            const float kn = in ? __half2float(nrm[lane]) : 0.f;
-            const float vn = in ? __half2float(nrm[kTile + lane]) : 0.f;
-            sm.nk[ns][32 * r + lane] = kn;
-            sm.nv[ns][32 * r + lane] = vn;
-            const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(vn));
-            if (lane == 0) sm.lg[ns][r] = max((int)(mx >> 23) - 126, -24);
+#pragma unroll 1
+    for (int t = 0; t < tiles + lag; ++t) {
+      if (t < tiles) {  // ---- keys of tile t
+        const uint32_t no = tile_no + t, st = no & 1, ns = no % kNormSlots;
+        const int rec0 = 4 * (tile0 + t), n = min(4, n_rec - rec0);  // records of the tile
+        if (!wait_warp(sm, &sm.ring_full[rk.slot], rk.phase)) return;
+        if (!wait_warp(sm, &sm.k_empty[st], ((no >> 1) & 1) ^ 1)) return;
+        const uint8_t* const w0 = ring + rk.slot * 4 * tbytes;
+        const uint8_t* w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = w0 + min(i, n - 1) * tbytes;
+#pragma unroll 1
+        for (int i = 0; i < n_steps; ++i)
+          unpack_keys(i ? k1 : k0, sm.lut, w, kbuf + st * kTileBytes, lane);
+        if (me < 4) {  // norms of record me: masked tokens 0
+          const __half* nrm = reinterpret_cast<const __half*>(w0 + me * tbytes + norm_off);
+          const bool in = (rec0 + me) * kTile + lane < len;
+          const float kn = in ? __half2float(nrm[lane]) : 0.f;
+          const float vn = in ? __half2float(nrm[kTile + lane]) : 0.f;
+          sm.nk[ns][32 * me + lane] = kn;
+          sm.nv[ns][32 * me + lane] = vn;
+          const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(vn));
+          const uint32_t kx = __reduce_max_sync(0xffffffffu, __float_as_uint(kn));
+          const uint32_t km =
+              __reduce_min_sync(0xffffffffu, in ? __float_as_uint(kn) : 0x7F800000u);
+          if (lane == 0) {
+            sm.lg[ns][me] = max((int)(mx >> 23) - 126, -24);
+            sm.kmax[ns][me] = __uint_as_float(kx);
+            sm.kmin[ns][me] = __uint_as_float(km);  // +inf without a token
           }
-          for (int hs = (uw + 2 * r) % kUnpackWarps; hs < n_half; hs += kUnpackWarps)
-            unpack_keys(sm, pl, w, hs, kbuf + st * kTileBytes, r, lane);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
-          ++rc;
-        } else if (uw == r) {
-          sm.nk[ns][32 * r + lane] = 0.f;
-          sm.nv[ns][32 * r + lane] = 0.f;
-          if (lane == 0) sm.lg[ns][r] = -24;
         }
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[st]);
-      if (!wait_warp(sm, &sm.v_empty[st], ph ^ 1)) return;
-      for (int r = 0; r < 4; ++r) {
-        if (4 * (tile0 + t) + r >= n_rec) break;
-        const uint32_t slot = rc % p.ring;
-        if (!wait_warp(sm, &sm.ring_full[slot], (rc / p.ring) & 1)) return;
-        const uint8_t* w = ring + (size_t)slot * p.slot_bytes;
-        for (int m = (uw + 2 * r) % kUnpackWarps; m < 16; m += kUnpackWarps)
-          unpack_values<BV>(sm, w, m, vbuf + st * kTileBytes, r, lane);
+        fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
-        ++rc;
+        if (lane == 0) mbar_arrive(&sm.k_full[st]);
+        rk.next(n_ring);
       }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[st]);
+      if (t >= lag) {  // ---- values of tile t - lag: 32 coordinate rows of one record each
+        const uint32_t no = tile_no + t - lag;
+        const int n = min(4, n_rec - 4 * (tile0 + t - lag));
+        if (!wait_warp(sm, &sm.v_empty, (no & 1) ^ 1)) return;
+        const uint8_t* const w0 = ring + rv.slot * 4 * tbytes + key_bytes;
+#pragma unroll 1
+        for (int j = kUnpackWarps - 1 - uw; j < 4 * n; j += kUnpackWarps) {
+          const int rec = j >> 2, row = 32 * (j & 3) + lane;
+          unpack_values<BV>(sm.lut, w0 + rec * tbytes + 4 * BV * row, (uint32_t)lane * 4u,
+                            vbuf + (rec >> 1) * kPanel + row * 128, 4u * (rec & 1),
+                            (uint32_t)lane & 7u);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.ring_empty[rv.slot]);
+          mbar_arrive(&sm.v_full);
+        }
+        rv.next(n_ring);
+      }
     }
+    tile_no += tiles;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.desc_empty[ds]);
   }
@@ -857,80 +975,112 @@ __device__ void unpack_role(const PrefixParams& p, MainSmem& sm, uint8_t* kbuf, 
 constexpr uint32_t kIdesc = (1u << 4) | (16u << 17) | (8u << 24);
 
 template <bool SPLIT>
-__device__ void mma_role(const PrefixParams& p, MainSmem& sm, const uint8_t* qbuf,
+__device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, const uint8_t* qbuf,
                          const uint8_t* kbuf, const uint8_t* vbuf, uint32_t tmem) {
-  uint32_t quse[2] = {0u, 0u}, tile_base = 0;
-  uint32_t items[2] = {0u, 0u}, segs[2] = {0u, 0u};  // P tiles consumed, segments, per stream
+  const bool elected = elect_one();
+  // phases: bit s of quse (query slot s), items and segs (stream s)
+  uint32_t quse = 0, items = 0, segs = 0, tile_base = 0;
   const uint64_t qd = smem_desc(smem_addr(qbuf)), kd = smem_desc(smem_addr(kbuf)),
                  vd = smem_desc(smem_addr(vbuf));
   constexpr uint64_t kTileD = kTileBytes >> 4, kPanelD = kPanel >> 4;
   for (uint32_t seg = 0;; ++seg) {
     const uint32_t ds = seg & 1;
-    if (!wait_on(sm, &sm.desc_full[ds], (seg >> 1) & 1)) return;
+    if (!wait_warp(sm, &sm.desc_full[ds], (seg >> 1) & 1)) return;
     const Desc& d = sm.desc[ds];
     if (d.stop) return;
     const bool shared = d.shared;
     const int tiles = d.tiles, n_items = shared ? 2 * tiles : tiles, q0 = d.qslot;
-    const int ksteps = (min(max(d.plan.n_ranks, 1), 64) + 7) / 8;
+    const int ksteps = (min(max(d.n_ranks, 1), 64) + 7) / 8;
     const bool both = shared || SPLIT;
-    for (int i = 0; i < (both ? 2 : 1); ++i) {
-      if (!wait_on(sm, &sm.q_full[q0 + i], quse[q0 + i] & 1)) return;
-      ++quse[q0 + i];
+#pragma unroll 1
+    for (int i = q0; i < q0 + (both ? 2 : 1); ++i) {
+      if (!wait_warp(sm, &sm.q_full[i], quse >> i & 1)) return;
+      quse ^= 1u << i;
     }
-    auto qk = [&](int j) -> bool {
-      const int s = j & 1, t = shared ? j >> 1 : j;
-      const uint32_t no = tile_base + t, st = no & 1;
-      if (!shared || s == 0)
-        if (!wait_on(sm, &sm.k_full[st], (no >> 1) & 1)) return false;
-      tc_fence_after();
-      for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-        const uint64_t a = qd + (uint64_t)(SPLIT ? part : q0 + (shared ? s : 0)) * kTileD;
-        for (int ks = 0; ks < ksteps; ++ks) {
-          const uint64_t o = (uint64_t)(ks >> 2) * kPanelD + (uint64_t)(ks & 3) * 2;
-          mma_ss(tmem + kColS + 128 * s, a + o, kd + st * kTileD + o, kIdesc, part > 0 || ks > 0);
+    // step j: P V of item j - 2, then Q K of item j (item = a stream's tile;
+    // items alternate between the streams)
+#pragma unroll 1
+    for (int j = 0; j < n_items + 2; ++j) {
+      const int s = j & 1;
+      if (j >= 2) {
+        const int i = j - 2, t = shared ? i >> 1 : i;
+        const uint32_t no = tile_base + t;
+        if (!wait_warp(sm, &sm.p_ready[s], items >> s & 1)) return;
+        items ^= 1u << s;
+        if (!shared || s == 0)
+          if (!wait_warp(sm, &sm.v_full, no & 1)) return;
+        const bool first = i < 2;
+        if (first) {  // the previous segment's O of this stream has been read
+          if (!wait_warp(sm, &sm.o_free[s], (segs >> s & 1) ^ 1)) return;
+          segs ^= 1u << s;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+          const uint32_t a = tmem + kColS + 128 * s + 16 * part;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            if (elected)
+              mma_ts(tmem + kColO + 128 * s, a + 32 * (ks >> 1) + 8 * (ks & 1),
+                   vd + (uint64_t)((ks >> 2) * kPanelD + (ks & 3) * 2), kIdesc,
+                   !first || part > 0 || ks > 0);
+        }
+        if (elected && (!shared || s == 1)) mma_commit(&sm.v_empty);
+        if (elected && (i + 2 >= n_items)) mma_commit(&sm.o_full[s]);
+      }
+      if (j < n_items) {
+        const int t = shared ? j >> 1 : j;
+        const uint32_t no = tile_base + t, st = no & 1;
+        if (!shared || s == 0)
+          if (!wait_warp(sm, &sm.k_full[st], (no >> 1) & 1)) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+          const uint64_t a = qd + (uint64_t)(SPLIT ? part : q0 + (shared ? s : 0)) * kTileD;
+          const uint64_t k = kd + st * kTileD;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            if (ks < ksteps) {
+              const uint64_t o = (uint64_t)((ks >> 2) * kPanelD + (ks & 3) * 2);
+              if (elected) mma_ss(tmem + kColS + 128 * s, a + o, k + o, kIdesc, part > 0 || ks > 0);
+            }
+        }
+        if (elected) mma_commit(&sm.s_full[s]);
+        if (elected && (!shared || s == 1)) mma_commit(&sm.k_empty[st]);
+        if (j == n_items - 1) {  // the segment's query rows are no longer needed
+          if (elected) mma_commit(&sm.q_empty[q0]);
+          if (elected && (both)) mma_commit(&sm.q_empty[q0 + 1]);
         }
       }
-      mma_commit(&sm.s_full[s]);
-      if (!shared || s == 1) mma_commit(&sm.k_empty[st]);
-      if (j == n_items - 1) {  // the segment's query rows are no longer needed
-        mma_commit(&sm.q_empty[q0]);
-        if (both) mma_commit(&sm.q_empty[q0 + 1]);
-      }
-      return true;
-    };
-    if (!qk(0)) return;
-    if (n_items > 1 && !qk(1)) return;
-    for (int j = 0; j < n_items; ++j) {
-      const int s = j & 1, t = shared ? j >> 1 : j;
-      const uint32_t no = tile_base + t, st = no & 1;
-      if (!wait_on(sm, &sm.p_ready[s], items[s] & 1)) return;
-      ++items[s];
-      if (!shared || s == 0)
-        if (!wait_on(sm, &sm.v_full[st], (no >> 1) & 1)) return;
-      const bool first = j < 2;
-      if (first) {  // the previous segment's O of this stream has been read
-        if (!wait_on(sm, &sm.o_free[s], (segs[s] & 1) ^ 1)) return;
-        ++segs[s];
-      }
-      tc_fence_after();
-      for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + kColO + 128 * s, tmem + kColS + 128 * s + 64 * part + 8 * ks,
-                 vd + st * kTileD + (uint64_t)(ks >> 2) * kPanelD + (uint64_t)(ks & 3) * 2, kIdesc,
-                 !first || part > 0 || ks > 0);
-      if (!shared || s == 1) mma_commit(&sm.v_empty[st]);
-      if (j + 2 >= n_items) mma_commit(&sm.o_full[s]);
-      else if (!qk(j + 2)) return;
     }
     tile_base += tiles;
-    mbar_arrive(&sm.desc_empty[ds]);
+    if (elected) mbar_arrive(&sm.desc_empty[ds]);
+  }
+}
+
+// 32 logits times their key norms; -inf from position `valid` on.
+__device__ __forceinline__ void scale_logits(float (&u)[32], const float4* nk4, int valid) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float4 f = nk4[e];
+    const float2 a = mul2(make_float2(u[4 * e], u[4 * e + 1]), make_float2(f.x, f.y));
+    const float2 b = mul2(make_float2(u[4 * e + 2], u[4 * e + 3]), make_float2(f.z, f.w));
+    u[4 * e] = a.x;
+    u[4 * e + 1] = a.y;
+    u[4 * e + 2] = b.x;
+    u[4 * e + 3] = b.y;
+  }
+  if (valid < 32) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e >= valid) u[e] = -INFINITY;
   }
 }
 
 // Softmax of stream s (one warpgroup, thread = query row): logits from TMEM,
 // running reference m and sum l, P back to TMEM, records at the end.
 template <bool SPLIT>
-__device__ void softmax_role(const PrefixParams& p, MainSmem& sm, uint32_t tmem, int s, int wq,
+__device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm, uint32_t tmem, int s, int wq,
                              int lane) {
   uint32_t items = 0, segs = 0, tile_base = 0;
   const uint32_t lane_addr = (uint32_t)(32 * wq) << 16;
@@ -958,86 +1108,101 @@ __device__ void softmax_role(const PrefixParams& p, MainSmem& sm, uint32_t tmem,
       if (!wait_warp(sm, &sm.s_full[s], items & 1)) return;
       if (active) {
         tc_fence_after();
-        float u[kTok];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(u) + 32 * c);
-        tmem_wait_ld();
-        // logits times key norms, the row's maximum
+        // pass 1: a bound of the row's logits, its largest product times the
+        // tile's largest (or, below zero, smallest) key norm. Both passes go over
+        // 32 columns at a time in loops that are not unrolled: with all 128
+        // columns unrolled the code of the roles outgrew the instruction cache
         const float4* nk4 = reinterpret_cast<const float4*>(sm.nk[ns]);
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+        const float4* nv4 = reinterpret_cast<const float4*>(sm.nv[ns]);
+        const int nvalid = len - (tile0 + t) * kTok;  // >= kTok but for the last tile
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float u[32];
+          tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(u));
+          tmem_wait_ld();
+          float a = mx, b = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < kTok / 4; ++c) {
-          const float4 f = nk4[c];
-          const float2 a = mul2(make_float2(u[4 * c], u[4 * c + 1]), make_float2(f.x, f.y));
-          const float2 b = mul2(make_float2(u[4 * c + 2], u[4 * c + 3]), make_float2(f.z, f.w));
-          u[4 * c] = a.x;
-          u[4 * c + 1] = a.y;
-          u[4 * c + 2] = b.x;
-          u[4 * c + 3] = b.y;
+          for (int e = 0; e < 32; e += 4) {
+            a = fmaxf(fmaxf(a, u[e]), u[e + 1]);
+            b = fmaxf(fmaxf(b, u[e + 2]), u[e + 3]);
+          }
+          mx = fmaxf(a, b);
         }
-        const int nv = len - (tile0 + t) * kTok;
-        if (nv < kTok) {  // the last tile: positions past the end
+        const int4 lg4 = *reinterpret_cast<const int4*>(sm.lg[ns]);
+        const float lg = (float)max(max(lg4.x, lg4.y), max(lg4.z, lg4.w));
+        const float4 kx4 = *reinterpret_cast<const float4*>(sm.kmax[ns]);
+        const float4 kn4 = *reinterpret_cast<const float4*>(sm.kmin[ns]);
+        const float kx = fmaxf(fmaxf(kx4.x, kx4.y), fmaxf(kx4.z, kx4.w));
+        const float kn = fminf(fminf(kn4.x, kn4.y), fminf(kn4.z, kn4.w));
+        float top = mx * (mx > 0.f ? kx : kn) * isc + lg;
+        // the reference moves only when a product would pass 2^kPTop (or on
+        // NaN); where the bound says it might, the exact maximum decides
+        bool move = valid && !(top - m <= kPTop);
+        if (__any_sync(0xffffffffu, move)) {
+          mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float u[32];
+            tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(u));
+            tmem_wait_ld();
+            scale_logits(u, nk4 + 8 * c, nvalid - 32 * c);
 #pragma unroll
-          for (int c = 0; c < kTok; ++c)
-            if (c >= nv) u[c] = -INFINITY;
+            for (int e = 0; e < 32; e += 2) mx = fmaxf(fmaxf(mx, u[e]), u[e + 1]);
+          }
+          top = mx * isc + lg;
+          move = valid && !(top - m <= kPTop);
         }
-#pragma unroll
-        for (int c = 0; c < kTok; c += 4) {
-          mx0 = fmaxf(fmaxf(mx0, u[c]), u[c + 1]);
-          mx1 = fmaxf(fmaxf(mx1, u[c + 2]), u[c + 3]);
-        }
-        const float top = fmaxf(mx0, mx1) * isc +
-                          (float)max(max(sm.lg[ns][0], sm.lg[ns][1]),
-                                     max(sm.lg[ns][2], sm.lg[ns][3]));
-        // the reference moves only when a product would pass 2^kPTop (or on NaN)
-        const bool move = valid && !(top - m <= kPTop);
         if (__any_sync(0xffffffffu, move)) {
           const float m_new = move ? top - kPSet : m;
           const float alpha = move ? ex2(m - m_new) : 1.f;  // 0 from -inf
           l *= alpha;
           if (i > 0) {  // O holds this segment's earlier tiles
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32(to + 32 * c, o);
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              uint32_t o[8];
+              tmem_ld8(to + 8 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(to + 32 * c, o);
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st8(to + 8 * c, o);
             }
           }
           m = m_new;
         }
-        const float4* nv4 = reinterpret_cast<const float4*>(sm.nv[ns]);
+        // pass 2: P = 2^(s - m) times the value norm, in place of the logits: the
+        // pairs of columns 32 c .. go to columns 32 c .. + 15 (low parts + 16 ..)
         const float2 isc2 = make_float2(isc, isc), nm2 = make_float2(-m, -m);
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float u[32];
+          tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(u));
+          tmem_wait_ld();
+          scale_logits(u, nk4 + 8 * c, nvalid - 32 * c);
+          uint32_t hi[16], lo[SPLIT ? 16 : 1];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t hi[32], lo[SPLIT ? 32 : 1];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int k = 64 * half + 4 * c;
-            const float4 f = nv4[16 * half + c];
-            float2 a = fma2(make_float2(u[k], u[k + 1]), isc2, nm2);
-            float2 b = fma2(make_float2(u[k + 2], u[k + 3]), isc2, nm2);
+          for (int e = 0; e < 8; ++e) {
+            const float4 f = nv4[8 * c + e];
+            float2 a = fma2(make_float2(u[4 * e], u[4 * e + 1]), isc2, nm2);
+            float2 b = fma2(make_float2(u[4 * e + 2], u[4 * e + 3]), isc2, nm2);
             a = make_float2(ex2(a.x), ex2(a.y));
             b = make_float2(ex2(b.x), ex2(b.y));
             l0 = add2(l0, a);
             l1 = add2(l1, b);
             a = mul2(a, make_float2(f.x, f.y));
             b = mul2(b, make_float2(f.z, f.w));
-            hi[2 * c] = pack_half2(a.x, a.y);
-            hi[2 * c + 1] = pack_half2(b.x, b.y);
+            hi[2 * e] = pack_half2(a.x, a.y);
+            hi[2 * e + 1] = pack_half2(b.x, b.y);
             if constexpr (SPLIT) {
-              const __half2 ha = *reinterpret_cast<const __half2*>(&hi[2 * c]);
-              const __half2 hb = *reinterpret_cast<const __half2*>(&hi[2 * c + 1]);
-              lo[2 * c] = pack_half2(a.x - __low2float(ha), a.y - __high2float(ha));
-              lo[2 * c + 1] = pack_half2(b.x - __low2float(hb), b.y - __high2float(hb));
+              const __half2 ha = *reinterpret_cast<const __half2*>(&hi[2 * e]);
+              const __half2 hb = *reinterpret_cast<const __half2*>(&hi[2 * e + 1]);
+              lo[2 * e] = pack_half2(a.x - __low2float(ha), a.y - __high2float(ha));
+              lo[2 * e + 1] = pack_half2(b.x - __low2float(hb), b.y - __high2float(hb));
             }
           }
-          tmem_st32(ts + 32 * half, hi);
-          if constexpr (SPLIT) tmem_st32(ts + 64 + 32 * half, lo);
+          tmem_st16(ts + 32 * c, hi);
+          if constexpr (SPLIT) tmem_st16(ts + 32 * c + 16, lo);
         }
         l += (l0.x + l0.y) + (l1.x + l1.y);
         tmem_wait_st();
@@ -1051,7 +1216,7 @@ __device__ void softmax_role(const PrefixParams& p, MainSmem& sm, uint32_t tmem,
       ++segs;
       if (active) {
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
           tmem_ld32(to + 32 * c, o);
@@ -1091,17 +1256,17 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
       mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.k_full[i], kUnpackWarps);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], kUnpackWarps);
-      mbar_init(&sm.v_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_ready[i], 4);
       mbar_init(&sm.o_full[i], 1);
       mbar_init(&sm.o_free[i], 4);
     }
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&sm.ring_full[i], 1);
+      mbar_init(&sm.ring_full[i], 1);  // one expect_tx for the tile's records
       mbar_init(&sm.ring_empty[i], kUnpackWarps);
     }
+    mbar_init(&sm.v_full, kUnpackWarps);
+    mbar_init(&sm.v_empty, 1);
     mbar_init(&sm.lut_full, 1);
     mbar_init(&sm.drain, 1);
     sm.fail = 0;
@@ -1114,7 +1279,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
     tmem_relinquish();
   }
   // operand columns and rows that no tile ever writes must be finite
-  for (uint32_t i = tid; i < 4 * kTileBytes / 16; i += kPThreads)
+  for (uint32_t i = tid; i < 3 * kTileBytes / 16; i += kPThreads)
     reinterpret_cast<uint4*>(kbuf)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async();
   tc_fence_before();
@@ -1122,20 +1287,20 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   grid_dep_wait();
-  // registers: 256 x 184 + 256 x 72 = 512 x 128
+  // registers: 256 x 112 + 512 x 64 = 768 x 80
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     softmax_role<SPLIT>(p, sm, tmem, warp >> 2, warp & 3, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == kCopyWarp) {
-      copy_role<SPLIT>(p, sm, qbuf, ring, lane);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == kWalkWarp) {
+      walk_role<SPLIT>(p, sm, qbuf, lane);
+    } else if (warp == kCopyWarp) {
+      copy_role(p, sm, ring, lane);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) {
-        mma_role<SPLIT>(p, sm, qbuf, kbuf, vbuf, tmem);
-        mma_commit(&sm.drain);  // nothing of this CTA's is in flight after it
-        (void)mbar_wait_bounded(&sm.drain, 0);
-      }
+      mma_role<SPLIT>(p, sm, qbuf, kbuf, vbuf, tmem);
+      if (elect_one()) mma_commit(&sm.drain);  // nothing of this CTA's is in flight after it
+      (void)mbar_wait_bounded(&sm.drain, 0);
       __syncwarp();
     } else {
       unpack_role<BV>(p, sm, kbuf, vbuf, ring, warp - kUnpackWarp0, lane);
@@ -1170,24 +1335,27 @@ __device__ __forceinline__ void merge_one(Merge& a, float2 ml, float4 o) {
   a.m = m;
 }
 
-// CTAs whose pieces may hold tiles of a unit: the CTA of position x.
-__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int n) {
-  int c = (int)(x * n / total);
-  while (c > 0 && cut(total, c, n) > x) --c;
-  while (c < n - 1 && cut(total, c + 1, n) <= x) ++c;
+// CTA whose piece holds position x of the cost line (cuts in shared memory).
+__device__ __forceinline__ int cta_of(const int64_t* cuts, int n, int64_t x) {
+  int c = 0;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (cuts[c + half] <= x) c += half;
+    n -= half;
+  }
   return c;
 }
 
 // Adds the records of one row of a unit: CTA c's piece at incidence c + idx,
 // `per` rows each; streams 0 and 1 at row and row + sub unless shared.
-__device__ __forceinline__ void merge_unit(Merge& acc, const PrefixParams& p, int64_t total,
-                                           int64_t start, int tiles, bool shared, int64_t idx,
-                                           const float2* ml, const float* o, int per, int row,
-                                           int sub, int part, int parts, int lane) {
-  if (tiles == 0) return;
-  const int w = shared ? kCostShared : kCostAlt;
-  const int c0 = cta_of(start + kCostSeg, total, p.n_ctas);
-  const int c1 = cta_of(start + kCostSeg + (int64_t)(tiles - 1) * w, total, p.n_ctas);
+__device__ __forceinline__ void merge_unit(Merge& acc, const int64_t* cuts, int n_cuts,
+                                           const Unit& u, const float2* ml, const float* o, int per,
+                                           int row, int sub, int part, int parts, int lane) {
+  if (u.tiles == 0) return;
+  const int w = u.shared ? kCostShared : kCostAlt;
+  const int64_t first = u.start + kCostSeg;
+  const int c0 = cta_of(cuts, n_cuts, first);
+  const int c1 = cta_of(cuts, n_cuts, first + (int64_t)(u.tiles - 1) * w);
   constexpr int kBatch = 4;
   for (int c = c0 + part; c <= c1; c += parts * kBatch) {
     float2 m2[kBatch][2];
@@ -1197,14 +1365,14 @@ __device__ __forceinline__ void merge_unit(Merge& acc, const PrefixParams& p, in
       const int cc = c + i * parts;
       int n = 0;
       if (cc <= c1)
-        n = tiles_before(cut(total, cc + 1, p.n_ctas), start, tiles, shared) -
-            tiles_before(cut(total, cc, p.n_ctas), start, tiles, shared);
+        n = tiles_before(cuts[cc + 1], u.start, u.tiles, u.shared) -
+            tiles_before(cuts[cc], u.start, u.tiles, u.shared);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         m2[i][s] = make_float2(-INFINITY, 0.f);
         o2[i][s] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n > s && !(shared && s)) {
-          const size_t at = (size_t)(cc + idx) * per + row + s * sub;
+        if (n > s && !(u.shared && s)) {
+          const size_t at = (size_t)(cc + u.idx) * per + row + s * sub;
           m2[i][s] = ml[at];
           o2[i][s] = reinterpret_cast<const float4*>(o + at * kHeadDim)[lane];
         }
@@ -1219,11 +1387,15 @@ __device__ __forceinline__ void merge_unit(Merge& acc, const PrefixParams& p, in
 
 __global__ void __launch_bounds__(kCombineWarps * 32) prefix_combine_kernel(const PrefixParams p) {
   __shared__ Merge part_sum[kCombineWarps][32];
+  extern __shared__ int64_t s_cuts[];  // [n_ctas + 1]
   __shared__ int s_g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.a.n_kv, h = blockIdx.x - b * p.a.n_kv;
   grid_dep_launch();
   grid_dep_wait();
+  const int64_t total = p.head->total;
+  const int n_cuts = (int)p.head->n_cuts;
+  for (int i = tid; i <= p.n_ctas; i += kCombineWarps * 32) s_cuts[i] = p.cuts[i];
   if (tid == 0) {
     int g = 0, len = p.a.n_groups + 1;
     while (len > 1) {
@@ -1236,18 +1408,15 @@ __global__ void __launch_bounds__(kCombineWarps * 32) prefix_combine_kernel(cons
   __syncthreads();
   const int g = s_g, parts = kCombineWarps / p.G;  // G <= 16
   const int head = warp / parts, part = warp % parts;
-  const int64_t total = p.head->total;
   Merge acc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   if (head < p.G && total > 0) {
-    if (g >= 0) {
-      const int rr = (b - p.gstart[g]) * p.G + head;
-      const Unit u = prefix_unit(p, g, h, rr / p.rows_unit);
-      merge_unit(acc, p, total, u.start, u.tiles, u.shared, u.idx, p.ml_p, p.o_p, 256,
-                 rr % p.rows_unit, 128, part, parts, lane);
+#pragma unroll 1
+    for (int k = g >= 0 ? 0 : 1; k < 2; ++k) {  // the prefix's records, then the sequence's own
+      const int rr = k ? 0 : (b - p.gstart[g]) * p.G + head;
+      const Unit u = k ? suffix_unit(p, b, h) : prefix_unit(p, g, h, rr / p.rows_unit);
+      merge_unit(acc, s_cuts, n_cuts, u, k ? p.ml_s : p.ml_p, k ? p.o_s : p.o_p,
+                 k ? 2 * p.G : 256, k ? head : rr % p.rows_unit, k ? p.G : 128, part, parts, lane);
     }
-    const Unit u = suffix_unit(p, b, h);
-    merge_unit(acc, p, total, u.start, u.tiles, false, u.idx, p.ml_s, p.o_s, 2 * p.G, head, p.G,
-               part, parts, lane);
   }
   if (parts > 1) {
     part_sum[warp][lane] = acc;
@@ -1338,7 +1507,7 @@ static cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t sm
 
 template <int BV, bool SPLIT>
 static cudaError_t launch_main(const PrefixParams& p, cudaStream_t st) {
-  const size_t smem = kMainTiles + sizeof(MainSmem) + (size_t)p.ring * p.slot_bytes;
+  const size_t smem = kMainTiles + sizeof(MainSmem) + (size_t)p.ring * 4 * p.tile_bytes;
   cudaError_t e = cudaFuncSetAttribute(prefix_main_kernel<BV, SPLIT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
@@ -1362,7 +1531,8 @@ static cudaError_t launch_all(const PrefixParams& p, cudaStream_t st) {
     default: e = cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefix_combine_kernel, p.a.batch * p.a.n_kv, kCombineWarps * 32, 0, p, st);
+  return launch_pdl(prefix_combine_kernel, p.a.batch * p.a.n_kv, kCombineWarps * 32,
+                    (size_t)(p.n_ctas + 1) * sizeof(int64_t), p, st);
 }
 
 cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -1379,6 +1549,7 @@ cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes,
   p.rows_unit = split ? 128 : 256;
   uint8_t* const s = static_cast<uint8_t*>(ws);
   p.head = reinterpret_cast<PfxHead*>(s + w.head);
+  p.cuts = reinterpret_cast<int64_t*>(s + w.cuts);
   p.gstart = reinterpret_cast<int32_t*>(s + w.gstart);
   p.gunit = reinterpret_cast<int32_t*>(s + w.gunit);
   p.gcost = reinterpret_cast<int64_t*>(s + w.gcost);
@@ -1391,10 +1562,9 @@ cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes,
   p.ml_s = reinterpret_cast<float2*>(s + w.ml_s);
   p.o_p = reinterpret_cast<float*>(s + w.o_p);
   p.o_s = reinterpret_cast<float*>(s + w.o_s);
-  p.slot_bytes = 512 * std::max(a.bits_k, a.bits_v) + 128;  // keys carry the norms; values'
-                                                            // last reads run past their words
-  p.ring = (int)std::min<size_t>(kMaxRing,
-                                 (kMaxSmem - kMainTiles - sizeof(MainSmem)) / p.slot_bytes);
+  // the unpacking reads up to two words past a record's code words
+  p.ring = (int)std::min<size_t>(
+      kMaxRing, (kMaxSmem - kMainTiles - sizeof(MainSmem)) / (4 * (size_t)p.tile_bytes));
   return split ? launch_all<true>(p, st) : launch_all<false>(p, st);
 }
 
