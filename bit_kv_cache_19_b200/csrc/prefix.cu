@@ -901,12 +901,15 @@ __device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm,
                          pl.bits_v == BV && plan_sched_ok(pl, lane);
     if (!plan_ok && uw == 0 && lane == 0) atomicOr(p.a.status, KVQ_FLAG_BAD_PLAN);
     const int n_half = plan_ok ? pl.n_half : 0;
+    // half steps: the widest (slowest) ones first, one to each warp; the rest, the
+    // narrowest, to the last warps, and the values' odd tasks to the first
+    const int hs1 = 2 * kUnpackWarps - 1 - uw;
     const KeyStep k0 = key_step(pl, uw < n_half ? uw : 0, lane);
-    const KeyStep k1 = key_step(pl, uw + kUnpackWarps < n_half ? uw + kUnpackWarps : 0, lane);
-    const int n_steps = (uw < n_half) + (uw + kUnpackWarps < n_half);
+    const KeyStep k1 = key_step(pl, hs1 < n_half ? hs1 : 0, lane);
+    const int n_steps = (uw < n_half) + (hs1 < n_half);
     const int n_rec = (d.len + kTile - 1) / kTile, key_bytes = 512 * p.a.bits_k;
     const int norm_off = key_bytes + 512 * BV;
-    const int me = uw >= kUnpackWarps - 4 ? uw - (kUnpackWarps - 4) : 4;  // a record's norms, or none
+    const int me = uw >= 3 && uw < 7 ? uw - 3 : 4;  // a record's norms, or none
     const int tiles = d.tiles, tile0 = d.tile0, len = d.len;
 #pragma unroll 1
     for (int t = 0; t < tiles + lag; ++t) {
@@ -950,7 +953,7 @@ __device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm,
         if (!wait_warp(sm, &sm.v_empty, (no & 1) ^ 1)) return;
         const uint8_t* const w0 = ring + rv.slot * 4 * tbytes + key_bytes;
 #pragma unroll 1
-        for (int j = kUnpackWarps - 1 - uw; j < 4 * n; j += kUnpackWarps) {
+        for (int j = uw; j < 4 * n; j += kUnpackWarps) {
           const int rec = j >> 2, row = 32 * (j & 3) + lane;
           unpack_values<BV>(sm.lut, w0 + rec * tbytes + 4 * BV * row, (uint32_t)lane * 4u,
                             vbuf + (rec >> 1) * kPanel + row * 128, 4u * (rec & 1),
