@@ -1316,7 +1316,11 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
 }
 
 // ------------------------------------------------------------------- combine
-constexpr int kCombineWarps = 16;
+// One CTA per (sequence, KV head), G x parts warps: `parts` warps share a query
+// head's records and merge through shared memory. Registers are held to 64 so
+// that two CTAs of 16 warps fit an SM; at 82 the 384 CTAs of a 48-sequence batch
+// ran in three waves and took 20 us instead of one.
+constexpr int kCombineMaxWarps = 32;
 
 // Running merge of records: lane holds coordinates 4 lane .. 4 lane + 3.
 struct Merge {
@@ -1349,8 +1353,8 @@ __device__ __forceinline__ int cta_of(const int64_t* cuts, int n, int64_t x) {
   return c;
 }
 
-// Adds the records of one row of a unit: CTA c's piece at incidence c + idx,
-// `per` rows each; streams 0 and 1 at row and row + sub unless shared.
+// Adds every parts-th record of one row of a unit: CTA c's piece is at incidence
+// c + idx, `per` rows each; streams 0 and 1 at row and row + sub unless shared.
 __device__ __forceinline__ void merge_unit(Merge& acc, const int64_t* cuts, int n_cuts,
                                            const Unit& u, const float2* ml, const float* o, int per,
                                            int row, int sub, int part, int parts, int lane) {
@@ -1359,78 +1363,66 @@ __device__ __forceinline__ void merge_unit(Merge& acc, const int64_t* cuts, int 
   const int64_t first = u.start + kCostSeg;
   const int c0 = cta_of(cuts, n_cuts, first);
   const int c1 = cta_of(cuts, n_cuts, first + (int64_t)(u.tiles - 1) * w);
+  const int two = u.shared ? 0 : 1, n = (c1 - c0 + 1) << two;  // candidate records
   constexpr int kBatch = 4;
-  for (int c = c0 + part; c <= c1; c += parts * kBatch) {
-    float2 m2[kBatch][2];
-    float4 o2[kBatch][2];
+#pragma unroll 1
+  for (int k = part; k < n; k += parts * kBatch) {
+    float2 m4[kBatch];
+    float4 o4[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int cc = c + i * parts;
-      int n = 0;
-      if (cc <= c1)
-        n = tiles_before(cuts[cc + 1], u.start, u.tiles, u.shared) -
-            tiles_before(cuts[cc], u.start, u.tiles, u.shared);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        m2[i][s] = make_float2(-INFINITY, 0.f);
-        o2[i][s] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n > s && !(u.shared && s)) {
-          const size_t at = (size_t)(cc + u.idx) * per + row + s * sub;
-          m2[i][s] = ml[at];
-          o2[i][s] = reinterpret_cast<const float4*>(o + at * kHeadDim)[lane];
-        }
+      const int kk = k + i * parts, c = c0 + (kk >> two), s = kk & two;
+      m4[i] = make_float2(-INFINITY, 0.f);
+      o4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (kk < n && tiles_before(cuts[c + 1], u.start, u.tiles, u.shared) -
+                            tiles_before(cuts[c], u.start, u.tiles, u.shared) > s) {
+        const size_t at = (size_t)(c + u.idx) * per + row + s * sub;
+        m4[i] = ml[at];
+        o4[i] = reinterpret_cast<const float4*>(o + at * kHeadDim)[lane];
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) merge_one(acc, m2[i][s], o2[i][s]);
+    for (int i = 0; i < kBatch; ++i) merge_one(acc, m4[i], o4[i]);
   }
 }
 
-__global__ void __launch_bounds__(kCombineWarps * 32) prefix_combine_kernel(const PrefixParams p) {
-  __shared__ Merge part_sum[kCombineWarps][32];
+__global__ void __launch_bounds__(kCombineMaxWarps * 32) prefix_combine_kernel(
+    const PrefixParams p, int parts) {
   extern __shared__ int64_t s_cuts[];  // [n_ctas + 1]
-  __shared__ int s_g;
+  __shared__ Merge part_sum[kCombineMaxWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.a.n_kv, h = blockIdx.x - b * p.a.n_kv;
   grid_dep_launch();
   grid_dep_wait();
-  const int64_t total = p.head->total;
+  for (int i = tid; i <= p.n_ctas; i += blockDim.x) s_cuts[i] = p.cuts[i];
+  const bool any = p.head->total > 0;
   const int n_cuts = (int)p.head->n_cuts;
-  for (int i = tid; i <= p.n_ctas; i += kCombineWarps * 32) s_cuts[i] = p.cuts[i];
-  if (tid == 0) {
-    int g = 0, len = p.a.n_groups + 1;
-    while (len > 1) {
-      const int half = len >> 1;
-      if (p.gstart[g + half] <= b) g += half;
-      len -= half;
-    }
-    s_g = g < p.a.n_groups && p.gstart[g] <= b ? g : -1;
+  int g = 0;
+  for (int len = p.a.n_groups + 1; len > 1;) {
+    const int half = len >> 1;
+    if (p.gstart[g + half] <= b) g += half;
+    len -= half;
   }
+  const bool grouped = g < p.a.n_groups && p.gstart[g] <= b;
+  const int head = warp / parts, part = warp - head * parts;
   __syncthreads();
-  const int g = s_g, parts = kCombineWarps / p.G;  // G <= 16
-  const int head = warp / parts, part = warp % parts;
   Merge acc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  if (head < p.G && total > 0) {
 #pragma unroll 1
-    for (int k = g >= 0 ? 0 : 1; k < 2; ++k) {  // the prefix's records, then the sequence's own
-      const int rr = k ? 0 : (b - p.gstart[g]) * p.G + head;
-      const Unit u = k ? suffix_unit(p, b, h) : prefix_unit(p, g, h, rr / p.rows_unit);
-      merge_unit(acc, s_cuts, n_cuts, u, k ? p.ml_s : p.ml_p, k ? p.o_s : p.o_p,
-                 k ? 2 * p.G : 256, k ? head : rr % p.rows_unit, k ? p.G : 128, part, parts, lane);
-    }
+  for (int k = grouped ? 0 : 1; k < 2 && any; ++k) {  // the prefix's records, then its own
+    const int rr = k ? 0 : (b - p.gstart[g]) * p.G + head;
+    const Unit u = k ? suffix_unit(p, b, h) : prefix_unit(p, g, h, rr / p.rows_unit);
+    merge_unit(acc, s_cuts, n_cuts, u, k ? p.ml_s : p.ml_p, k ? p.o_s : p.o_p, k ? 2 * p.G : 256,
+               k ? head : rr % p.rows_unit, k ? p.G : 128, part, parts, lane);
   }
   if (parts > 1) {
     part_sum[warp][lane] = acc;
     __syncthreads();
-    if (part == 0)
-      for (int i = 1; i < parts && head < p.G; ++i) {
-        const Merge x = part_sum[warp + i][lane];
-        merge_one(acc, make_float2(x.m, x.l), x.o);
-      }
+    if (part) return;
+    for (int i = 1; i < parts; ++i) {
+      const Merge x = part_sum[warp + i][lane];
+      merge_one(acc, make_float2(x.m, x.l), x.o);
+    }
   }
-  if (head >= p.G || part) return;
   // o = s . H o / (128 l): coordinates 4 lane + i, distances 1, 2 in the lane,
   // 4 .. 64 across lanes
   float y[4];
@@ -1492,9 +1484,9 @@ size_t prefix_workspace_bytes(int batch, int n_q, int n_kv, int n_groups) {
   return pfx_layout(batch, n_q, n_kv, n_groups, n).bytes;
 }
 
-template <typename K>
-static cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem,
-                              const PrefixParams& p, cudaStream_t st) {
+template <typename K, typename... A>
+static cudaError_t launch_pdl(cudaStream_t st, K kernel, unsigned grid, unsigned block, size_t smem,
+                              const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
@@ -1505,7 +1497,7 @@ static cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t sm
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int BV, bool SPLIT>
@@ -1514,13 +1506,13 @@ static cudaError_t launch_main(const PrefixParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(prefix_main_kernel<BV, SPLIT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefix_main_kernel<BV, SPLIT>, p.n_ctas, kPThreads, smem, p, st);
+  return launch_pdl(st, prefix_main_kernel<BV, SPLIT>, p.n_ctas, kPThreads, smem, p);
 }
 
 template <bool SPLIT>
 static cudaError_t launch_all(const PrefixParams& p, cudaStream_t st) {
-  cudaError_t e = launch_pdl(prefix_prep_kernel<SPLIT>, 1 + p.a.batch * p.a.n_kv, kPrepThreads, 0,
-                             p, st);
+  cudaError_t e =
+      launch_pdl(st, prefix_prep_kernel<SPLIT>, 1 + p.a.batch * p.a.n_kv, kPrepThreads, 0, p);
   if (e != cudaSuccess) return e;
   switch (p.a.bits_v) {
     case 1: e = launch_main<1, SPLIT>(p, st); break;
@@ -1534,8 +1526,12 @@ static cudaError_t launch_all(const PrefixParams& p, cudaStream_t st) {
     default: e = cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefix_combine_kernel, p.a.batch * p.a.n_kv, kCombineWarps * 32,
-                    (size_t)(p.n_ctas + 1) * sizeof(int64_t), p, st);
+  // warps per query head: up to 8, so many that about 32 warps per SM are at work
+  // and a CTA has at most 32
+  const int parts = std::max(1, std::min({8, kCombineMaxWarps / p.G,
+                                          32 * p.n_ctas / (p.a.batch * p.a.n_q)}));
+  return launch_pdl(st, prefix_combine_kernel, p.a.batch * p.a.n_kv, 32 * p.G * parts,
+                    (size_t)(p.n_ctas + 1) * sizeof(int64_t), p, parts);
 }
 
 cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes, cudaStream_t st) {
