@@ -76,8 +76,22 @@ struct PfxHead {
   int64_t n_cuts;   // CTAs that get a piece of the cost line
   int64_t pad;
 };
+// First unit of a CTA's piece: a sequence (suffix) or a group, KV head, row tile.
+struct alignas(16) PfxFirst {
+  int32_t suffix, i, h, rt;
+};
+// Prefix rows of a sequence: unit of KV head 0 (-1: no prefix), row tiles per KV
+// head, first row in the group.
+struct alignas(16) PfxRow {
+  int32_t unit0, nrt, row0, pad;
+};
+// A unit's pieces: CTAs c0 .. c1 of the cost line.
+struct alignas(16) PfxUnit {
+  int64_t start;
+  int32_t tiles, shared, c0, c1, pad[2];
+};
 struct PfxLayout {
-  size_t head, cuts, gstart, gunit, gcost, scost, isc_p, isc_s, q_p, q_s, ml_p, ml_s, o_p, o_s, bytes;
+  size_t head, cuts, first, row, unit_p, unit_s, gstart, gunit, gcost, scost, isc_p, isc_s, q_p, q_s, ml_p, ml_s, o_p, o_s, bytes;
 };
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -98,6 +112,10 @@ static PfxLayout pfx_layout(int batch, int n_q, int n_kv, int n_groups, int n_ct
   };
   w.head = take(sizeof(PfxHead));
   w.cuts = take((size_t)(n_ctas + 1) * 8);
+  w.first = take((size_t)n_ctas * sizeof(PfxFirst));
+  w.row = take((size_t)batch * sizeof(PfxRow));
+  w.unit_p = take(units * sizeof(PfxUnit));
+  w.unit_s = take((size_t)batch * n_kv * sizeof(PfxUnit));
   w.gstart = take((size_t)(n_groups + 1) * 4);
   w.gunit = take((size_t)(n_groups + 1) * 4);
   w.gcost = take((size_t)(n_groups + 1) * 8);
@@ -120,6 +138,9 @@ struct PrefixParams {
   int rows_unit;  // 256 or 128 rows per prefix unit
   PfxHead* head;
   int64_t* cuts;  // [n_ctas + 1] first position of each CTA's piece
+  PfxFirst* first;  // [n_ctas]
+  PfxRow* row;      // [batch]
+  PfxUnit *unit_p, *unit_s;
   int32_t *gstart, *gunit;
   int64_t *gcost, *scost;
   float *isc_p, *isc_s;
@@ -174,6 +195,7 @@ struct PrepSmem {
   RotTables rot;
   int gstart[kPfxMaxGroups + 1];
   int gunit[kPfxMaxGroups + 1];
+  int64_t gcost[kPfxMaxGroups + 1];
   int64_t warp_sum[8];
   alignas(16) float row[8][kHeadDim];
 };
@@ -239,10 +261,24 @@ __device__ __forceinline__ int64_t block_sum_before(int64_t x, int64_t* warp_sum
   return before + inc - x;
 }
 
-__device__ void prep_schedule(const PrefixParams& p, PrepSmem& sm) {
+// Largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
+__device__ __forceinline__ int last_at(const int64_t* a, int n, int64_t x) {
+  int lo = 0;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (a[lo + half] <= x) lo += half;
+    n -= half;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void prep_schedule(const PrefixParams& p, PrepSmem& sm) {
   const int tid = threadIdx.x, n = p.a.n_groups;
   uint32_t flags = 0;
   int64_t base = 0;
+  // the first lengths are on their way while the groups are summed
+  int raw_len = tid < p.a.batch ? p.a.len[tid] : 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += kPrepThreads) {
     const int i = i0 + tid;
     int64_t c = 0;
@@ -256,18 +292,19 @@ __device__ void prep_schedule(const PrefixParams& p, PrepSmem& sm) {
     int64_t total;
     const int64_t before = block_sum_before(c, sm.warp_sum, total);
     if (i < n) {
-      p.gcost[i] = base + before;
+      sm.gcost[i] = p.gcost[i] = base + before;
       p.gstart[i] = sm.gstart[i];
       p.gunit[i] = sm.gunit[i];
     }
     base += total;
   }
   const int64_t suffix0 = base;
+#pragma unroll 1
   for (int i0 = 0; i0 < p.a.batch; i0 += kPrepThreads) {
     const int i = i0 + tid;
     int64_t c = 0;
     if (i < p.a.batch) {
-      const int raw = p.a.len[i];
+      const int raw = i0 ? p.a.len[i] : raw_len;
       if (raw > p.a.max_len) flags |= KVQ_FLAG_CAPACITY;
       c = seq_cost(tiles_of(clamp_len(raw, p.a.max_len)), p.a.n_kv);
     }
@@ -276,10 +313,6 @@ __device__ void prep_schedule(const PrefixParams& p, PrepSmem& sm) {
     if (i < p.a.batch) p.scost[i] = base + before;
     base += total;
   }
-  // no more pieces than tiles of the dearer kind; the CTAs past them get none
-  const int64_t pieces = min((int64_t)p.n_ctas, max((int64_t)1, base / kCostShared));
-  for (int i = tid; i <= p.n_ctas; i += kPrepThreads)
-    p.cuts[i] = i < pieces ? base * i / pieces : base;
   if (tid == 0) {
     p.gcost[n] = suffix0;
     p.gstart[n] = sm.gstart[n];
@@ -287,7 +320,34 @@ __device__ void prep_schedule(const PrefixParams& p, PrepSmem& sm) {
     p.scost[p.a.batch] = base;
     p.head->total = base;
     p.head->suffix0 = suffix0;
-    p.head->n_cuts = pieces;
+  }
+  __syncthreads();  // the sums are read below
+  // no more pieces than tiles of the dearer kind; the CTAs past them get none
+  const int64_t pieces = min((int64_t)p.n_ctas, max((int64_t)1, base / kCostShared));
+  if (tid == 0) p.head->n_cuts = pieces;
+#pragma unroll 1
+  for (int c = tid; c <= p.n_ctas; c += kPrepThreads) {
+    const int64_t x = c < pieces ? base * c / pieces : base;
+    p.cuts[c] = x;
+    if (c >= p.n_ctas || x >= base) continue;
+    PfxFirst f;
+    f.suffix = x >= suffix0;
+    f.rt = 0;
+    if (f.suffix) {
+      f.i = last_at(p.scost, p.a.batch, x);
+      const int64_t cost =
+          seq_cost(tiles_of(clamp_len(p.a.len[f.i], p.a.max_len)), p.a.n_kv) / p.a.n_kv;
+      f.h = (int)((x - p.scost[f.i]) / cost);
+    } else {
+      f.i = last_at(sm.gcost, n, x);
+      const int rows = (sm.gstart[f.i + 1] - sm.gstart[f.i]) * p.G;
+      const GroupCost gc =
+          group_cost(rows, tiles_of(clamp_len(p.a.pre_len[f.i], p.a.max_pre)), p.rows_unit);
+      const int64_t d = x - sm.gcost[f.i];
+      f.h = (int)(d / gc.block);
+      f.rt = (int)min((d - f.h * gc.block) / gc.full, (int64_t)gc.nrt - 1);
+    }
+    p.first[c] = f;
   }
   if (flags) atomicOr(p.a.status, flags);
 }
@@ -385,6 +445,17 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixP
     }
   }
   const bool grouped = g < n && sm.gstart[g] <= b;
+  // units without tiles have no piece: the merge finds these entries
+  if (tid == 0) p.unit_s[bh] = PfxUnit{0, 0, 0, 0, -1, {0, 0}};
+  if (grouped && b == sm.gstart[g])
+    for (int u = tid; u < (sm.gunit[g + 1] - sm.gunit[g]) / p.a.n_kv; u += kPrepThreads)
+      p.unit_p[sm.gunit[g] + h * ((sm.gunit[g + 1] - sm.gunit[g]) / p.a.n_kv) + u] =
+          PfxUnit{0, 0, 0, 0, -1, {0, 0}};
+  if (h == 0 && tid == 0) {
+    const int rows = grouped ? (sm.gstart[g + 1] - sm.gstart[g]) * p.G : 0;
+    p.row[b] = PfxRow{grouped ? sm.gunit[g] : -1, (rows + p.rows_unit - 1) / p.rows_unit,
+                      grouped ? (b - sm.gstart[g]) * p.G : 0, 0};
+  }
   uint32_t sign[4] = {0u, 0u, 0u, 0u};
   const Plan* held = nullptr;
   bool ok = false;
@@ -430,7 +501,7 @@ struct alignas(16) Desc {  // one segment: a run of tiles of one unit
   float* o;
   const float* isc;
   unsigned long long base[32];  // page bases of the first 32 records (0: refused)
-  int suffix, row, n_ranks;     // cache map and its row
+  int suffix, row;              // cache map and its row
   int stop, shared, rows, tiles, tile0, len, b0, row0, h, qslot, sub;
 };
 
@@ -538,30 +609,6 @@ __device__ __forceinline__ int warp_last_le(const int64_t* a, int n, int64_t x, 
     n = min(step, n - k * step);
   }
   return lo;
-}
-
-// The unit with cost at position x of the cost line.
-__device__ __forceinline__ Unit unit_at(const PrefixParams& p, int64_t x, int64_t suffix0,
-                                        int lane) {
-  const bool suffix = x >= suffix0;
-  const int i = warp_last_le(suffix ? p.scost : p.gcost, suffix ? p.a.batch : p.a.n_groups, x, lane);
-  if (suffix) {
-    Unit u = suffix_unit(p, i, 0);
-    while (u.start + u.cost <= x && u.h + 1 < p.a.n_kv) {
-      ++u.h;
-      u.start += u.cost;
-      ++u.idx;
-    }
-    return u;
-  }
-  const int rows = (p.gstart[i + 1] - p.gstart[i]) * p.G;
-  const GroupCost c =
-      group_cost(rows, tiles_of(clamp_len(p.a.pre_len[i], p.a.max_pre)), p.rows_unit);
-  int64_t d = x - p.gcost[i];
-  int h = 0;
-  for (; d >= c.block && h + 1 < p.a.n_kv; ++h) d -= c.block;
-  const int rt = (int)min(d / c.full, (int64_t)c.nrt - 1);
-  return prefix_unit(p, i, h, rt);
 }
 
 // What a lane needs to unpack one half step (<= 4 blocks of width W) of a
@@ -725,27 +772,42 @@ template <bool SPLIT>
 __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, uint8_t* qbuf,
                                           int lane) {
   const int64_t suffix0 = p.head->suffix0;
+  const int n_cuts = (int)p.head->n_cuts;
   const int64_t x0 = p.cuts[blockIdx.x], x1 = p.cuts[blockIdx.x + 1];
+  PfxFirst f = p.first[blockIdx.x];  // of a CTA without a piece: not used
   uint32_t seg = 0;                // segments
   uint32_t quse[2] = {0u, 0u};     // segments that used each query slot
   int qnext = 0;
   bool ok = true;
-  int64_t x = x0;
+  bool more = x0 < x1;
 #pragma unroll 1
-  while (ok && x < x1) {
-    const Unit u = unit_at(p, x, suffix0, lane);
-    x = u.start + u.cost;
+  while (ok && more) {
+    const Unit u = f.suffix ? suffix_unit(p, f.i, f.h) : prefix_unit(p, f.i, f.h, f.rt);
     const int t0 = tiles_before(x0, u.start, u.tiles, u.shared);
     const int t1 = tiles_before(x1, u.start, u.tiles, u.shared);
-    if (u.cost == 0) break;
-    if (t0 >= t1) continue;
-    const int row = u.suffix ? u.b : u.g, n_rec = (u.len + kTile - 1) / kTile;
+    const int row = f.i, n_rec = (u.len + kTile - 1) / kTile;
     const Plan* const plan = p.a.plans[u.b] + u.h;
-    const int n_ranks = plan->n_ranks;
     unsigned long long base = 0;
-    if (4 * t0 + lane < n_rec)
+    if (t0 < t1 && 4 * t0 + lane < n_rec)
       base = (unsigned long long)(uintptr_t)page_base(u.suffix ? p.a.own : p.a.pre, row,
                                                       4 * t0 + lane);
+    // the next unit with a cost, if this CTA's piece goes on
+    const int64_t x = u.start + u.cost;
+    more = x < x1;
+    if (more) {
+      const bool cross = !f.suffix && x >= suffix0;
+      if (f.suffix) {
+        if (++f.h == p.a.n_kv) f.i = warp_last_le(p.scost, p.a.batch, x, lane);
+      } else if (cross) {
+        f.i = warp_last_le(p.scost, p.a.batch, x, lane);
+      } else if (++f.rt == u.nrt) {
+        f.rt = 0;
+        if (++f.h == p.a.n_kv) f.i = warp_last_le(p.gcost, p.a.n_groups, x, lane);
+      }
+      if (cross || f.h == p.a.n_kv) f.h = f.rt = 0;
+      f.suffix = x >= suffix0;
+    }
+    if (t0 >= t1) continue;
     const uint32_t ds = seg & 1;
     ok = wait_warp(sm, &sm.desc_empty[ds], ((seg >> 1) & 1) ^ 1);
     if (!ok) break;
@@ -761,7 +823,6 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
       d.isc = u.suffix ? p.isc_s : p.isc_p;
       d.suffix = u.suffix;
       d.row = row;
-      d.n_ranks = n_ranks;
       d.stop = 0;
       d.shared = u.shared;
       d.rows = u.rows;
@@ -799,6 +860,14 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
       quse[1] += s == 1;
     }
     if (!both) qnext ^= 1;
+    if (t0 == 0) {  // the unit starts here: where its pieces lie, for the merge
+      const int w = u.shared ? kCostShared : kCostAlt;
+      const int c1 = warp_last_le(p.cuts, n_cuts,
+                                  u.start + kCostSeg + (int64_t)(u.tiles - 1) * w, lane);
+      if (lane == 0)
+        (u.suffix ? p.unit_s : p.unit_p)[u.idx] =
+            PfxUnit{u.start, u.tiles, u.shared, (int)blockIdx.x, c1, {0, 0}};
+    }
   }
   if (ok) {  // the end of the CTA's work
     const uint32_t ds = seg & 1;
@@ -993,7 +1062,7 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
     if (d.stop) return;
     const bool shared = d.shared;
     const int tiles = d.tiles, n_items = shared ? 2 * tiles : tiles, q0 = d.qslot;
-    const int ksteps = (min(max(d.n_ranks, 1), 64) + 7) / 8;
+    const int ksteps = (min(max(d.plan.n_ranks, 1), 64) + 7) / 8;
     const bool both = shared || SPLIT;
 #pragma unroll 1
     for (int i = q0; i < q0 + (both ? 2 : 1); ++i) {
@@ -1321,6 +1390,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
 // that two CTAs of 16 warps fit an SM; at 82 the 384 CTAs of a 48-sequence batch
 // ran in three waves and took 20 us instead of one.
 constexpr int kCombineMaxWarps = 32;
+constexpr int kMaxCtas = 256;  // of the main grid
 
 // Running merge of records: lane holds coordinates 4 lane .. 4 lane + 3.
 struct Merge {
@@ -1342,28 +1412,59 @@ __device__ __forceinline__ void merge_one(Merge& a, float2 ml, float4 o) {
   a.m = m;
 }
 
-// CTA whose piece holds position x of the cost line (cuts in shared memory).
-__device__ __forceinline__ int cta_of(const int64_t* cuts, int n, int64_t x) {
-  int c = 0;
-  while (n > 1) {
-    const int half = n >> 1;
-    if (cuts[c + half] <= x) c += half;
-    n -= half;
+__global__ void __launch_bounds__(kCombineMaxWarps * 32) prefix_combine_kernel(
+    const PrefixParams p, int parts) {
+  extern __shared__ int64_t s_cuts[];  // [n_ctas + 1]
+  __shared__ Merge part_sum[kCombineMaxWarps][32];
+  __shared__ uint32_t s_list[3][2 * kMaxCtas];
+  __shared__ int s_n[3];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / p.a.n_kv, h = blockIdx.x - b * p.a.n_kv;
+  const int head = warp / parts, part = warp - head * parts;
+  grid_dep_launch();
+  grid_dep_wait();
+  // three rounds of loads: tables; the prefix's unit; the records
+  const PfxRow pr = p.row[b];
+  const PfxUnit us = p.unit_s[blockIdx.x];
+  const Plan* const pl = p.a.plans[b] + h;
+  for (int i = tid; i <= p.n_ctas; i += blockDim.x) s_cuts[i] = p.cuts[i];
+  // the prefix's units of the first and the last query head (rows of a sequence
+  // may straddle two), and the suffix's
+  const int ra = pr.row0 / p.rows_unit, rb = (pr.row0 + p.G - 1) / p.rows_unit;
+  const int unit_a = pr.unit0 + h * pr.nrt + ra;
+  PfxUnit ua{0, 0, 0, 0, -1, {0, 0}}, ub = ua;
+  if (pr.unit0 >= 0) {
+    ua = p.unit_p[unit_a];
+    if (rb != ra) ub = p.unit_p[unit_a + 1];
   }
-  return c;
-}
-
-// Adds every parts-th record of one row of a unit: CTA c's piece is at incidence
-// c + idx, `per` rows each; streams 0 and 1 at row and row + sub unless shared.
-__device__ __forceinline__ void merge_unit(Merge& acc, const int64_t* cuts, int n_cuts,
-                                           const Unit& u, const float2* ml, const float* o, int per,
-                                           int row, int sub, int part, int parts, int lane) {
-  if (u.tiles == 0) return;
-  const int w = u.shared ? kCostShared : kCostAlt;
-  const int64_t first = u.start + kCostSeg;
-  const int c0 = cta_of(cuts, n_cuts, first);
-  const int c1 = cta_of(cuts, n_cuts, first + (int64_t)(u.tiles - 1) * w);
-  const int two = u.shared ? 0 : 1, n = (c1 - c0 + 1) << two;  // candidate records
+  const uint32_t sg = pl->v_sign[lane >> 3] >> (4 * (lane & 7));
+  __syncthreads();
+  // lists of their records, one warp each: (CTA c, stream s) as 2 (c + unit) + s,
+  // CTA c's piece being at incidence c + unit; a shared unit's row is in one
+  // stream, so its second stream's records are left out
+  const int n_warps = p.G * parts;
+#pragma unroll 1
+  for (int l = warp; l < 3; l += n_warps) {
+    const PfxUnit u = l == 0 ? ua : l == 1 ? ub : us;
+    const int inc = l == 2 ? (int)blockIdx.x : unit_a + l, two = u.shared ? 0 : 1;
+    int n = 0;
+#pragma unroll 1
+    for (int k0 = 0; k0 < (u.c1 - u.c0 + 1) << two; k0 += 32) {
+      const int k = k0 + lane, c = u.c0 + (k >> two), s = k & two;
+      const bool has = k < (u.c1 - u.c0 + 1) << two &&
+                       tiles_before(s_cuts[c + 1], u.start, u.tiles, u.shared) -
+                               tiles_before(s_cuts[c], u.start, u.tiles, u.shared) > s;
+      const uint32_t got = __ballot_sync(0xffffffffu, has);
+      if (has) s_list[l][n + __popc(got & ((1u << lane) - 1u))] = 2 * (c + inc) + s;
+      n += __popc(got);
+    }
+    if (lane == 0) s_n[l] = n;
+  }
+  __syncthreads();
+  Merge acc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int rr = pr.row0 + head, lp = rr / p.rows_unit - ra, row = rr % p.rows_unit;
+  const bool shared = lp ? ub.shared : ua.shared;
+  const int n_p = s_n[lp], n = n_p + s_n[2];
   constexpr int kBatch = 4;
 #pragma unroll 1
   for (int k = part; k < n; k += parts * kBatch) {
@@ -1371,48 +1472,20 @@ __device__ __forceinline__ void merge_unit(Merge& acc, const int64_t* cuts, int 
     float4 o4[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int kk = k + i * parts, c = c0 + (kk >> two), s = kk & two;
+      const int kk = k + i * parts;
       m4[i] = make_float2(-INFINITY, 0.f);
       o4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (kk < n && tiles_before(cuts[c + 1], u.start, u.tiles, u.shared) -
-                            tiles_before(cuts[c], u.start, u.tiles, u.shared) > s) {
-        const size_t at = (size_t)(c + u.idx) * per + row + s * sub;
-        m4[i] = ml[at];
-        o4[i] = reinterpret_cast<const float4*>(o + at * kHeadDim)[lane];
+      if (kk < n) {
+        const bool suf = kk >= n_p;
+        const uint32_t e = suf ? s_list[2][kk - n_p] : s_list[lp][kk];
+        const size_t at = suf ? (size_t)e * p.G + head
+                              : (size_t)(e >> 1) * 256 + (shared ? 0 : (e & 1) * 128) + row;
+        m4[i] = (suf ? p.ml_s : p.ml_p)[at];
+        o4[i] = reinterpret_cast<const float4*>((suf ? p.o_s : p.o_p) + at * kHeadDim)[lane];
       }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) merge_one(acc, m4[i], o4[i]);
-  }
-}
-
-__global__ void __launch_bounds__(kCombineMaxWarps * 32) prefix_combine_kernel(
-    const PrefixParams p, int parts) {
-  extern __shared__ int64_t s_cuts[];  // [n_ctas + 1]
-  __shared__ Merge part_sum[kCombineMaxWarps][32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.x / p.a.n_kv, h = blockIdx.x - b * p.a.n_kv;
-  grid_dep_launch();
-  grid_dep_wait();
-  for (int i = tid; i <= p.n_ctas; i += blockDim.x) s_cuts[i] = p.cuts[i];
-  const bool any = p.head->total > 0;
-  const int n_cuts = (int)p.head->n_cuts;
-  int g = 0;
-  for (int len = p.a.n_groups + 1; len > 1;) {
-    const int half = len >> 1;
-    if (p.gstart[g + half] <= b) g += half;
-    len -= half;
-  }
-  const bool grouped = g < p.a.n_groups && p.gstart[g] <= b;
-  const int head = warp / parts, part = warp - head * parts;
-  __syncthreads();
-  Merge acc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 1
-  for (int k = grouped ? 0 : 1; k < 2 && any; ++k) {  // the prefix's records, then its own
-    const int rr = k ? 0 : (b - p.gstart[g]) * p.G + head;
-    const Unit u = k ? suffix_unit(p, b, h) : prefix_unit(p, g, h, rr / p.rows_unit);
-    merge_unit(acc, s_cuts, n_cuts, u, k ? p.ml_s : p.ml_p, k ? p.o_s : p.o_p, k ? 2 * p.G : 256,
-               k ? head : rr % p.rows_unit, k ? p.G : 128, part, parts, lane);
   }
   if (parts > 1) {
     part_sum[warp][lane] = acc;
@@ -1446,10 +1519,8 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) prefix_combine_kernel(
       y[i] = upper ? x - y[i] : y[i] + x;
     }
   }
-  const Plan& pl = p.a.plans[b][h];
   // an empty row gives 0; a NaN sum stays NaN
   const float inv = acc.l == 0.f ? 0.f : 1.f / (128.f * acc.l);
-  const uint32_t sg = pl.v_sign[lane >> 3] >> (4 * (lane & 7));
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = ((sg >> i) & 1u ? -y[i] : y[i]) * inv;
   const size_t at = ((size_t)b * p.a.n_q + h * p.G + head) * kHeadDim + 4 * lane;
@@ -1467,14 +1538,14 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) prefix_combine_kernel(
 }
 
 // ------------------------------------------------------------------ launchers
-constexpr int kFallbackCtas = 256;  // CTAs when no device answers (size queries)
+constexpr int kFallbackCtas = kMaxCtas;  // CTAs when no device answers (size queries)
 
 static int main_ctas(cudaError_t* err) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   *err = e;
-  return e == cudaSuccess ? sms : kFallbackCtas;
+  return e == cudaSuccess ? std::min(sms, kMaxCtas) : kFallbackCtas;
 }
 
 size_t prefix_workspace_bytes(int batch, int n_q, int n_kv, int n_groups) {
@@ -1549,6 +1620,10 @@ cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes,
   uint8_t* const s = static_cast<uint8_t*>(ws);
   p.head = reinterpret_cast<PfxHead*>(s + w.head);
   p.cuts = reinterpret_cast<int64_t*>(s + w.cuts);
+  p.first = reinterpret_cast<PfxFirst*>(s + w.first);
+  p.row = reinterpret_cast<PfxRow*>(s + w.row);
+  p.unit_p = reinterpret_cast<PfxUnit*>(s + w.unit_p);
+  p.unit_s = reinterpret_cast<PfxUnit*>(s + w.unit_s);
   p.gstart = reinterpret_cast<int32_t*>(s + w.gstart);
   p.gunit = reinterpret_cast<int32_t*>(s + w.gunit);
   p.gcost = reinterpret_cast<int64_t*>(s + w.gcost);
