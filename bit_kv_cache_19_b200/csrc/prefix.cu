@@ -1052,9 +1052,10 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
   const bool elected = elect_one();
   // phases: bit s of quse (query slot s), items and segs (stream s)
   uint32_t quse = 0, items = 0, segs = 0, tile_base = 0;
-  const uint64_t qd = smem_desc(smem_addr(qbuf)), kd = smem_desc(smem_addr(kbuf)),
-                 vd = smem_desc(smem_addr(vbuf));
-  constexpr uint64_t kTileD = kTileBytes >> 4, kPanelD = kPanel >> 4;
+  // low words of the operand descriptors (addresses in units of 16 bytes)
+  const uint32_t qd = desc_lo(smem_addr(qbuf)), kd = desc_lo(smem_addr(kbuf)),
+                 vd = desc_lo(smem_addr(vbuf));
+  constexpr uint32_t kTileD = kTileBytes >> 4, kPanelD = kPanel >> 4;
   for (uint32_t seg = 0;; ++seg) {
     const uint32_t ds = seg & 1;
     if (!wait_warp(sm, &sm.desc_full[ds], (seg >> 1) & 1)) return;
@@ -1062,7 +1063,7 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
     if (d.stop) return;
     const bool shared = d.shared;
     const int tiles = d.tiles, n_items = shared ? 2 * tiles : tiles, q0 = d.qslot;
-    const int ksteps = (min(max(d.plan.n_ranks, 1), 64) + 7) / 8;
+    const uint32_t ksteps = (min(max(d.plan.n_ranks, 1), 64) + 7) / 8;
     const bool both = shared || SPLIT;
 #pragma unroll 1
     for (int i = q0; i < q0 + (both ? 2 : 1); ++i) {
@@ -1087,18 +1088,21 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
           segs ^= 1u << s;
         }
         tc_fence_after();
+        if (elected) {
 #pragma unroll 1
-        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-          const uint32_t a = tmem + kColS + 128 * s + 16 * part;
+          for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+            const uint32_t a = tmem + kColS + 128 * s + 16 * part, o = tmem + kColO + 128 * s;
+            if (first && part == 0) mma_ts<false>(o, a, vd, kIdesc);
+            else mma_ts<true>(o, a, vd, kIdesc);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            if (elected)
-              mma_ts(tmem + kColO + 128 * s, a + 32 * (ks >> 1) + 8 * (ks & 1),
-                   vd + (uint64_t)((ks >> 2) * kPanelD + (ks & 3) * 2), kIdesc,
-                   !first || part > 0 || ks > 0);
+            for (uint32_t ks = 1; ks < 8; ++ks)
+              mma_ts<true>(o, a + 32 * (ks >> 1) + 8 * (ks & 1),
+                           vd + (ks >> 2) * kPanelD + (ks & 3) * 2, kIdesc);
+          }
+          if (!shared || s == 1) mma_commit(&sm.v_empty);
+          if (i + 2 >= n_items) mma_commit(&sm.o_full[s]);
         }
-        if (elected && (!shared || s == 1)) mma_commit(&sm.v_empty);
-        if (elected && (i + 2 >= n_items)) mma_commit(&sm.o_full[s]);
+        __syncwarp();
       }
       if (j < n_items) {
         const int t = shared ? j >> 1 : j;
@@ -1106,23 +1110,28 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
         if (!shared || s == 0)
           if (!wait_warp(sm, &sm.k_full[st], (no >> 1) & 1)) return;
         tc_fence_after();
+        if (elected) {
+          const uint32_t d = tmem + kColS + 128 * s, k = kd + st * kTileD;
 #pragma unroll 1
-        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-          const uint64_t a = qd + (uint64_t)(SPLIT ? part : q0 + (shared ? s : 0)) * kTileD;
-          const uint64_t k = kd + st * kTileD;
+          for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+            const uint32_t a = qd + (SPLIT ? part : q0 + (shared ? s : 0)) * kTileD;
+            if (part == 0) mma_ss<false>(d, a, k, kIdesc);
+            else mma_ss<true>(d, a, k, kIdesc);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            if (ks < ksteps) {
-              const uint64_t o = (uint64_t)((ks >> 2) * kPanelD + (ks & 3) * 2);
-              if (elected) mma_ss(tmem + kColS + 128 * s, a + o, k + o, kIdesc, part > 0 || ks > 0);
-            }
+            for (uint32_t ks = 1; ks < 8; ++ks)
+              if (ks < ksteps) {
+                const uint32_t o = (ks >> 2) * kPanelD + (ks & 3) * 2;
+                mma_ss<true>(d, a + o, k + o, kIdesc);
+              }
+          }
+          mma_commit(&sm.s_full[s]);
+          if (!shared || s == 1) mma_commit(&sm.k_empty[st]);
+          if (j == n_items - 1) {  // the segment's query rows are no longer needed
+            mma_commit(&sm.q_empty[q0]);
+            if (both) mma_commit(&sm.q_empty[q0 + 1]);
+          }
         }
-        if (elected) mma_commit(&sm.s_full[s]);
-        if (elected && (!shared || s == 1)) mma_commit(&sm.k_empty[st]);
-        if (j == n_items - 1) {  // the segment's query rows are no longer needed
-          if (elected) mma_commit(&sm.q_empty[q0]);
-          if (elected && (both)) mma_commit(&sm.q_empty[q0 + 1]);
-        }
+        __syncwarp();
       }
     }
     tile_base += tiles;
