@@ -510,10 +510,7 @@ struct alignas(128) MainSmem {
   Desc desc[2];
   alignas(16) float nk[kNormSlots][kTok];
   alignas(16) float nv[kNormSlots][kTok];
-  // per record: the value norms are below 2^lg; bounds of the key norms
-  alignas(16) int lg[kNormSlots][4];
-  alignas(16) float kmax[kNormSlots][4];
-  alignas(16) float kmin[kNormSlots][4];
+  int lg[kNormSlots][4];  // per record: the value norms are below 2^lg
   unsigned long long desc_full[2], desc_empty[2], ring_full[kMaxRing], ring_empty[kMaxRing];
   unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full, v_empty;
   unsigned long long s_full[2], p_ready[2], o_full[2], o_free[2], lut_full, drain;
@@ -649,21 +646,22 @@ __device__ __forceinline__ void unpack_keys(const KeyStep& k, const uint8_t* lut
       const uint32_t* a = reinterpret_cast<const uint32_t*>(w[r] + k.src);
       v[r] = funnel_r(a[0], a[1], sh) << 7;
     }
+    // every lookup before any store: the compiler cannot tell that the tile and
+    // the table do not overlap, and would hold each store's later lookups back
+    uint32_t x[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t x[4];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        x[r] = *reinterpret_cast<const uint32_t*>(lut + ((v[r] & m7) | lb));
-        v[r] >>= w2;
+        x[i][r] = *reinterpret_cast<const uint32_t*>(lut + ((v[r] & m7) | lb));
+        v[r] >>= w2;  // what falls below bit 7 is masked
       }
-      if (store) {
+    if (store) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          *reinterpret_cast<uint32_t*>(to + r * 4096 + i * 1024) = x[r];
-      }
-      // v keeps its code bits 7 places up, so the shift must not pull bits in
-      // from below bit 7: they are masked by m7
+          *reinterpret_cast<uint32_t*>(to + r * 4096 + i * 1024) = x[i][r];
     }
     return;
   }
@@ -672,28 +670,30 @@ __device__ __forceinline__ void unpack_keys(const KeyStep& k, const uint8_t* lut
                                                         : 0x3C00u + 2u * (uint32_t)((1 << W) - 2));
 #pragma unroll 1
   for (int r = 0; r < 4; r += 2) {
+    uint32_t x[2][4];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const uint8_t* src = r ? w[2 + q] : w[q];
       const uint32_t* a = reinterpret_cast<const uint32_t*>(src + k.src);
       const uint32_t a1 = a[1], hi = W > 4 ? funnel_r(a1, a[2], sh) : 0u;
       const unsigned long long v = ((unsigned long long)hi << 32) | funnel_r(a[0], a1, sh);
-      uint32_t x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t f = (uint32_t)(v >> (w2 * i));
         if (W <= 5)
-          x[i] = *reinterpret_cast<const uint32_t*>(tab + 4u * (f & mask));
+          x[q][i] = *reinterpret_cast<const uint32_t*>(tab + 4u * (f & mask));
         else
-          x[i] = *reinterpret_cast<const uint16_t*>(tab + 2u * (f & (mask >> W))) |
-                 ((uint32_t)*reinterpret_cast<const uint16_t*>(
-                      tab + 2u * ((f >> W) & (mask >> W))) << 16);
+          x[q][i] = *reinterpret_cast<const uint16_t*>(tab + 2u * (f & (mask >> W))) |
+                    ((uint32_t)*reinterpret_cast<const uint16_t*>(
+                         tab + 2u * ((f >> W) & (mask >> W))) << 16);
       }
-      if (store) {
+    }
+    if (store) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint32_t*>(to + (r + q) * 4096 + i * 1024) = x[i];
-      }
+          *reinterpret_cast<uint32_t*>(to + (r + q) * 4096 + i * 1024) = x[q][i];
     }
   }
 }
@@ -735,9 +735,9 @@ __device__ __forceinline__ void unpack_values(const uint8_t* lut, const uint8_t*
   uint32_t w[BV + 1];
   load_words<BV>(src, w);
   constexpr uint32_t mask = (1u << (2 * BV)) - 1u;
+  uint32_t x[4][4];  // every lookup before any store, as in unpack_keys
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t x[4];
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int o = (8 * c + 2 * i) * BV, k = o >> 5, s = o & 31;
@@ -746,22 +746,25 @@ __device__ __forceinline__ void unpack_values(const uint8_t* lut, const uint8_t*
         const uint32_t lb = lane4 | (BV == 1 ? 0x4000u : BV == 2 ? 0x2000u : 0u);
         const uint32_t v = spill ? funnel_r(w[k], w[k + 1], (s - 7) & 31)
                            : s >= 7 ? w[k] >> ((s - 7) & 31) : w[k] << ((7 - s) & 31);
-        x[c] = *reinterpret_cast<const uint32_t*>(lut + ((v & (mask << 7)) | lb));
+        x[i][c] = *reinterpret_cast<const uint32_t*>(lut + ((v & (mask << 7)) | lb));
       } else {
         const uint32_t v = spill ? funnel_r(w[k], w[k + 1], s) : w[k] >> s;
         if constexpr (BV <= 5) {
-          x[c] = *reinterpret_cast<const uint32_t*>(lut + (BV == 4 ? 0x2800u : 0x2C00u) +
-                                                    4u * (v & mask));
+          x[i][c] = *reinterpret_cast<const uint32_t*>(lut + (BV == 4 ? 0x2800u : 0x2C00u) +
+                                                       4u * (v & mask));
         } else {
           const uint8_t* tab = lut + 0x3C00u + 2u * (uint32_t)((1 << BV) - 2);
           constexpr uint32_t m1 = (1u << BV) - 1u;
-          x[c] = *reinterpret_cast<const uint16_t*>(tab + 2u * (v & m1)) |
-                 ((uint32_t)*reinterpret_cast<const uint16_t*>(tab + 2u * ((v >> BV) & m1)) << 16);
+          x[i][c] =
+              *reinterpret_cast<const uint16_t*>(tab + 2u * (v & m1)) |
+              ((uint32_t)*reinterpret_cast<const uint16_t*>(tab + 2u * ((v >> BV) & m1)) << 16);
         }
       }
     }
-    *reinterpret_cast<uint4*>(dst + (((chunk0 + i) ^ sw) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(dst + (((chunk0 + i) ^ sw) << 4)) =
+        make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
 }
 
 // ---- the roles of the main kernel
@@ -1002,14 +1005,7 @@ __device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm,
           sm.nk[ns][32 * me + lane] = kn;
           sm.nv[ns][32 * me + lane] = vn;
           const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(vn));
-          const uint32_t kx = __reduce_max_sync(0xffffffffu, __float_as_uint(kn));
-          const uint32_t km =
-              __reduce_min_sync(0xffffffffu, in ? __float_as_uint(kn) : 0x7F800000u);
-          if (lane == 0) {
-            sm.lg[ns][me] = max((int)(mx >> 23) - 126, -24);
-            sm.kmax[ns][me] = __uint_as_float(kx);
-            sm.kmin[ns][me] = __uint_as_float(km);  // +inf without a token
-          }
+          if (lane == 0) sm.lg[ns][me] = max((int)(mx >> 23) - 126, -24);
         }
         fence_proxy_async();
         __syncwarp();
@@ -1189,71 +1185,14 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
       if (!wait_warp(sm, &sm.s_full[s], items & 1)) return;
       if (active) {
         tc_fence_after();
-        // pass 1: a bound of the row's logits, its largest product times the
-        // tile's largest (or, below zero, smallest) key norm. Both passes go over
-        // 32 columns at a time in loops that are not unrolled: with all 128
-        // columns unrolled the code of the roles outgrew the instruction cache
+        // 32 columns (one record) at a time, in a loop that is not unrolled: with
+        // all 128 columns unrolled the code of the roles outgrew the instruction
+        // cache. P = 2^(s - m) times the value norm goes in place of the logits:
+        // the pairs of columns 32 c .. to columns 32 c .. + 15 (low parts + 16 ..)
         const float4* nk4 = reinterpret_cast<const float4*>(sm.nk[ns]);
         const float4* nv4 = reinterpret_cast<const float4*>(sm.nv[ns]);
         const int nvalid = len - (tile0 + t) * kTok;  // >= kTok but for the last tile
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float u[32];
-          tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(u));
-          tmem_wait_ld();
-          float a = mx, b = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            a = fmaxf(fmaxf(a, u[e]), u[e + 1]);
-            b = fmaxf(fmaxf(b, u[e + 2]), u[e + 3]);
-          }
-          mx = fmaxf(a, b);
-        }
-        const int4 lg4 = *reinterpret_cast<const int4*>(sm.lg[ns]);
-        const float lg = (float)max(max(lg4.x, lg4.y), max(lg4.z, lg4.w));
-        const float4 kx4 = *reinterpret_cast<const float4*>(sm.kmax[ns]);
-        const float4 kn4 = *reinterpret_cast<const float4*>(sm.kmin[ns]);
-        const float kx = fmaxf(fmaxf(kx4.x, kx4.y), fmaxf(kx4.z, kx4.w));
-        const float kn = fminf(fminf(kn4.x, kn4.y), fminf(kn4.z, kn4.w));
-        float top = mx * (mx > 0.f ? kx : kn) * isc + lg;
-        // the reference moves only when a product would pass 2^kPTop (or on
-        // NaN); where the bound says it might, the exact maximum decides
-        bool move = valid && !(top - m <= kPTop);
-        if (__any_sync(0xffffffffu, move)) {
-          mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float u[32];
-            tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(u));
-            tmem_wait_ld();
-            scale_logits(u, nk4 + 8 * c, nvalid - 32 * c);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx = fmaxf(fmaxf(mx, u[e]), u[e + 1]);
-          }
-          top = mx * isc + lg;
-          move = valid && !(top - m <= kPTop);
-        }
-        if (__any_sync(0xffffffffu, move)) {
-          const float m_new = move ? top - kPSet : m;
-          const float alpha = move ? ex2(m - m_new) : 1.f;  // 0 from -inf
-          l *= alpha;
-          if (i > 0) {  // O holds this segment's earlier tiles
-#pragma unroll 1
-            for (int c = 0; c < 16; ++c) {
-              uint32_t o[8];
-              tmem_ld8(to + 8 * c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st8(to + 8 * c, o);
-            }
-          }
-          m = m_new;
-        }
-        // pass 2: P = 2^(s - m) times the value norm, in place of the logits: the
-        // pairs of columns 32 c .. go to columns 32 c .. + 15 (low parts + 16 ..)
-        const float2 isc2 = make_float2(isc, isc), nm2 = make_float2(-m, -m);
+        const float2 isc2 = make_float2(isc, isc);
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -1261,6 +1200,50 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
           tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(u));
           tmem_wait_ld();
           scale_logits(u, nk4 + 8 * c, nvalid - 32 * c);
+          float mx = fmaxf(u[0], u[1]), mx1 = fmaxf(u[2], u[3]);
+#pragma unroll
+          for (int e = 4; e < 32; e += 4) {
+            mx = fmaxf(fmaxf(mx, u[e]), u[e + 1]);
+            mx1 = fmaxf(fmaxf(mx1, u[e + 2]), u[e + 3]);
+          }
+          // the reference, a whole number, moves only when a product would pass
+          // 2^kPTop (or on NaN): O, l and this tile's earlier P are scaled by a
+          // power of two
+          const float top = fmaxf(mx, mx1) * isc + (float)sm.lg[ns][c];
+          const bool move = valid && !(top - m <= kPTop) && nvalid > 32 * c;
+          if (__any_sync(0xffffffffu, move)) {
+            const float m_new = move ? ceilf(top) - kPSet : m;
+            const float alpha = move ? ex2(m - m_new) : 1.f;  // 0 from -inf
+            l *= alpha;
+            l0 = mul2(l0, make_float2(alpha, alpha));
+            l1 = mul2(l1, make_float2(alpha, alpha));
+            if (i > 0) {  // O holds this segment's earlier tiles
+#pragma unroll 1
+              for (int k = 0; k < 16; ++k) {
+                uint32_t o[8];
+                tmem_ld8(to + 8 * k, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st8(to + 8 * k, o);
+              }
+            }
+            const __half2 ah = __float2half2_rn(alpha);
+#pragma unroll 1
+            for (int k = 0; k < 4 * c; ++k) {  // columns 0 .. 31 of each earlier record
+              uint32_t o[8];
+              tmem_ld8(ts + 8 * k, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), ah);
+                o[e] = *reinterpret_cast<const uint32_t*>(&x);
+              }
+              tmem_st8(ts + 8 * k, o);
+            }
+            m = m_new;
+          }
+          const float2 nm2 = make_float2(-m, -m);
           uint32_t hi[16], lo[SPLIT ? 16 : 1];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
