@@ -665,35 +665,52 @@ __device__ __forceinline__ void unpack_keys(const KeyStep& k, const uint8_t* lut
     }
     return;
   }
-  // widths 4, 5: one pair table; wider: two single-code lookups
-  const uint8_t* tab = lut + (W == 4 ? 0x2800u : W == 5 ? 0x2C00u
-                                                        : 0x3C00u + 2u * (uint32_t)((1 << W) - 2));
+  if (W <= 5) {  // one pair table, at most 40 bits
+    const uint8_t* tab = lut + (W == 4 ? 0x2800u : 0x2C00u);
+    uint32_t lo[4], hi[4], x[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t* a = reinterpret_cast<const uint32_t*>(w[r] + k.src);
+      const uint32_t a1 = a[1];
+      lo[r] = funnel_r(a[0], a1, sh);
+      hi[r] = funnel_r(a1, a[2], sh);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        x[i][r] = *reinterpret_cast<const uint32_t*>(
+            tab + 4u * (funnel_r(lo[r], hi[r], w2 * i) & mask));
+    if (store) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<uint32_t*>(to + r * 4096 + i * 1024) = x[i][r];
+    }
+    return;
+  }
+  // wider: two single-code lookups
+  const uint8_t* tab = lut + 0x3C00u + 2u * (uint32_t)((1 << W) - 2);
+  const uint32_t m1 = mask >> W;
 #pragma unroll 1
-  for (int r = 0; r < 4; r += 2) {
-    uint32_t x[2][4];
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t* a = reinterpret_cast<const uint32_t*>(
+        (r == 0 ? w[0] : r == 1 ? w[1] : r == 2 ? w[2] : w[3]) + k.src);
+    const uint32_t a1 = a[1];
+    const unsigned long long v =
+        ((unsigned long long)funnel_r(a1, a[2], sh) << 32) | funnel_r(a[0], a1, sh);
+    uint32_t x[4];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint8_t* src = r ? w[2 + q] : w[q];
-      const uint32_t* a = reinterpret_cast<const uint32_t*>(src + k.src);
-      const uint32_t a1 = a[1], hi = W > 4 ? funnel_r(a1, a[2], sh) : 0u;
-      const unsigned long long v = ((unsigned long long)hi << 32) | funnel_r(a[0], a1, sh);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t f = (uint32_t)(v >> (w2 * i));
-        if (W <= 5)
-          x[q][i] = *reinterpret_cast<const uint32_t*>(tab + 4u * (f & mask));
-        else
-          x[q][i] = *reinterpret_cast<const uint16_t*>(tab + 2u * (f & (mask >> W))) |
-                    ((uint32_t)*reinterpret_cast<const uint16_t*>(
-                         tab + 2u * ((f >> W) & (mask >> W))) << 16);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t f = (uint32_t)(v >> (w2 * i));
+      x[i] = *reinterpret_cast<const uint16_t*>(tab + 2u * (f & m1)) |
+             ((uint32_t)*reinterpret_cast<const uint16_t*>(tab + 2u * ((f >> W) & m1)) << 16);
     }
     if (store) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint32_t*>(to + (r + q) * 4096 + i * 1024) = x[q][i];
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint32_t*>(to + r * 4096 + i * 1024) = x[i];
     }
   }
 }
@@ -1135,33 +1152,29 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
   }
 }
 
-// 32 logits times their key norms; -inf from position `valid` on.
-__device__ __forceinline__ void scale_logits(float (&u)[32], const float4* nk4, int valid) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float4 f = nk4[e];
-    const float2 a = mul2(make_float2(u[4 * e], u[4 * e + 1]), make_float2(f.x, f.y));
-    const float2 b = mul2(make_float2(u[4 * e + 2], u[4 * e + 3]), make_float2(f.z, f.w));
-    u[4 * e] = a.x;
-    u[4 * e + 1] = a.y;
-    u[4 * e + 2] = b.x;
-    u[4 * e + 3] = b.y;
-  }
-  if (valid < 32) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (e >= valid) u[e] = -INFINITY;
-  }
-}
-
-// Softmax of stream s (one warpgroup, thread = query row): logits from TMEM,
-// running reference m and sum l, P back to TMEM, records at the end.
+// Softmax of stream s (one warpgroup, 32 rows per warp). A chunk of 32 columns
+// (one record) is held like a matrix fragment: lane (g, q) = (lane / 4, lane mod
+// 4) has rows g + 8 k (k < 4) and columns 8 j + 2 q + (0, 1) (j < 4), so that a
+// lane loads 8 key and 8 value norms per chunk; with a row per lane it would load
+// 32 of each, and those loads alone took 2,000 shared-memory cycles per tile of
+// 256 rows.
 template <bool SPLIT>
-__device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm, uint32_t tmem, int s, int wq,
-                             int lane) {
+__device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm, uint32_t tmem,
+                                             int s, int wq, int lane) {
   uint32_t items = 0, segs = 0, tile_base = 0;
   const uint32_t lane_addr = (uint32_t)(32 * wq) << 16;
   const uint32_t ts = tmem + lane_addr + kColS + 128 * s, to = tmem + lane_addr + kColO + 128 * s;
+  const int g = lane >> 2, q = lane & 3;
+  // value of row `lane`, from the lane (lane mod 8, 0) that holds it as row 8 k + g
+  auto by_row = [&](const float (&v)[4]) -> float {
+    float r = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = __shfl_sync(0xffffffffu, v[k], (lane & 7) * 4);
+      if (lane >> 3 == k) r = x;
+    }
+    return r;
+  };
   for (uint32_t seg = 0;; ++seg) {
     const uint32_t ds = seg & 1;
     if (!wait_warp(sm, &sm.desc_full[ds], (seg >> 1) & 1)) return;
@@ -1170,70 +1183,102 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
     const bool shared = d.shared;
     const int tiles = d.tiles, n = shared ? tiles : (tiles - s + 1) / 2;
     const int rows = shared ? min(128, d.rows - 128 * s) : d.rows;
-    const int row = 32 * wq + lane;  // in this stream's tile
-    const bool active = 32 * wq < rows, valid = row < rows;  // the warp has rows; this is one
-    const int rr = d.row0 + (shared ? 128 * s : 0) + min(row, rows - 1);
-    const int qi = (d.b0 + rr / p.G) * p.a.n_q + d.h * p.G + rr % p.G;
-    const float isc = active ? d.isc[qi] : 1.f;
+    const bool active = 32 * wq < rows;  // the warp has rows
+    float isc[4], m[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 32 * wq + g + 8 * k;  // in this stream's tile
+      const int rr = d.row0 + (shared ? 128 * s : 0) + min(row, rows - 1);
+      isc[k] = active ? d.isc[(d.b0 + rr / p.G) * p.a.n_q + d.h * p.G + rr % p.G] : 1.f;
+      // a row past the unit's has no reference to move: its numbers go nowhere
+      m[k] = row < rows ? -INFINITY : INFINITY;
+      l[k] = 0.f;
+    }
     const int len = d.len, tile0 = d.tile0;
-    float* const rec_o = d.o + (size_t)(s * d.sub + row) * kHeadDim;
-    float2* const rec_ml = d.ml + s * d.sub + row;
-    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
     for (int i = 0; i < n; ++i, ++items) {
       const int t = shared ? i : 2 * i + s;
       const uint32_t ns = (tile_base + t) % kNormSlots;
       if (!wait_warp(sm, &sm.s_full[s], items & 1)) return;
       if (active) {
         tc_fence_after();
-        // 32 columns (one record) at a time, in a loop that is not unrolled: with
-        // all 128 columns unrolled the code of the roles outgrew the instruction
-        // cache. P = 2^(s - m) times the value norm goes in place of the logits:
-        // the pairs of columns 32 c .. to columns 32 c .. + 15 (low parts + 16 ..)
-        const float4* nk4 = reinterpret_cast<const float4*>(sm.nk[ns]);
-        const float4* nv4 = reinterpret_cast<const float4*>(sm.nv[ns]);
         const int nvalid = len - (tile0 + t) * kTok;  // >= kTok but for the last tile
-        const float2 isc2 = make_float2(isc, isc);
-        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+        // chunks in a loop that is not unrolled: with all 128 columns unrolled the
+        // code of the roles outgrew the instruction cache. P = 2^(s - m) times the
+        // value norm goes in place of the logits: the pairs of columns 32 c .. to
+        // columns 32 c .. + 15 (low parts + 16 ..)
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          float u[32];
-          tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(u));
-          tmem_wait_ld();
-          scale_logits(u, nk4 + 8 * c, nvalid - 32 * c);
-          float mx = fmaxf(u[0], u[1]), mx1 = fmaxf(u[2], u[3]);
+          uint32_t v[2][16];
+          tmem_ld_frag(ts + 32 * c, v[0]);
+          tmem_ld_frag(ts + (16u << 16) + 32 * c, v[1]);
+          const float2* nk2 = reinterpret_cast<const float2*>(&sm.nk[ns][32 * c + 2 * q]);
+          const float2* nv2 = reinterpret_cast<const float2*>(&sm.nv[ns][32 * c + 2 * q]);
+          const float lg = (float)sm.lg[ns][c];
+          const float2 nk[4] = {nk2[0], nk2[4], nk2[8], nk2[12]};
+          tmem_wait_ld16(v[0]);
+          tmem_wait_ld16(v[1]);
+          float2 u[4][4];  // [row k][column group j]: logits times key norms
+          float top[4];
+          bool move = false;
 #pragma unroll
-          for (int e = 4; e < 32; e += 4) {
-            mx = fmaxf(fmaxf(mx, u[e]), u[e + 1]);
-            mx1 = fmaxf(fmaxf(mx1, u[e + 2]), u[e + 3]);
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int e = 4 * j + 2 * (k & 1);
+              u[k][j] = mul2(make_float2(__uint_as_float(v[k >> 1][e]),
+                                         __uint_as_float(v[k >> 1][e + 1])), nk[j]);
+            }
+          }
+          if (nvalid < 32 * c + 32) {  // the last tile: positions past the end
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (32 * c + 8 * j + 2 * q >= nvalid) u[k][j].x = -INFINITY;
+                if (32 * c + 8 * j + 2 * q + 1 >= nvalid) u[k][j].y = -INFINITY;
+              }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = fmaxf(fmaxf(u[k][0].x, u[k][0].y), u[k][1].x);
+            const float b = fmaxf(fmaxf(u[k][1].y, u[k][2].x), u[k][2].y);
+            top[k] = fmaxf(fmaxf(a, b), fmaxf(u[k][3].x, u[k][3].y)) * isc[k] + lg;
+            move |= 32 * wq + g + 8 * k < rows && !(top[k] - m[k] <= kPTop);
           }
           // the reference, a whole number, moves only when a product would pass
           // 2^kPTop (or on NaN): O, l and this tile's earlier P are scaled by a
           // power of two
-          const float top = fmaxf(mx, mx1) * isc + (float)sm.lg[ns][c];
-          const bool move = valid && !(top - m <= kPTop) && nvalid > 32 * c;
-          if (__any_sync(0xffffffffu, move)) {
-            const float m_new = move ? ceilf(top) - kPSet : m;
-            const float alpha = move ? ex2(m - m_new) : 1.f;  // 0 from -inf
-            l *= alpha;
-            l0 = mul2(l0, make_float2(alpha, alpha));
-            l1 = mul2(l1, make_float2(alpha, alpha));
+          if (nvalid > 32 * c && __any_sync(0xffffffffu, move)) {
+            float alpha[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
+              top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
+              const bool mv = !(top[k] - m[k] <= kPTop);
+              const float m_new = mv ? ceilf(top[k]) - kPSet : m[k];
+              alpha[k] = mv ? ex2(m[k] - m_new) : 1.f;  // 0 from -inf
+              l[k] *= alpha[k];
+              m[k] = m_new;
+            }
+            const float ar = by_row(alpha);
             if (i > 0) {  // O holds this segment's earlier tiles
 #pragma unroll 1
               for (int k = 0; k < 16; ++k) {
                 uint32_t o[8];
                 tmem_ld8(to + 8 * k, o);
-                tmem_wait_ld();
+                tmem_wait_ld8(o);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ar);
                 tmem_st8(to + 8 * k, o);
               }
             }
-            const __half2 ah = __float2half2_rn(alpha);
+            const __half2 ah = __float2half2_rn(ar);
 #pragma unroll 1
             for (int k = 0; k < 4 * c; ++k) {  // columns 0 .. 31 of each earlier record
               uint32_t o[8];
               tmem_ld8(ts + 8 * k, o);
-              tmem_wait_ld();
+              tmem_wait_ld8(o);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), ah);
@@ -1241,34 +1286,35 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
               }
               tmem_st8(ts + 8 * k, o);
             }
-            m = m_new;
           }
-          const float2 nm2 = make_float2(-m, -m);
-          uint32_t hi[16], lo[SPLIT ? 16 : 1];
+          uint32_t hi[2][8], lo[2][SPLIT ? 8 : 1];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 f = nv4[8 * c + e];
-            float2 a = fma2(make_float2(u[4 * e], u[4 * e + 1]), isc2, nm2);
-            float2 b = fma2(make_float2(u[4 * e + 2], u[4 * e + 3]), isc2, nm2);
-            a = make_float2(ex2(a.x), ex2(a.y));
-            b = make_float2(ex2(b.x), ex2(b.y));
-            l0 = add2(l0, a);
-            l1 = add2(l1, b);
-            a = mul2(a, make_float2(f.x, f.y));
-            b = mul2(b, make_float2(f.z, f.w));
-            hi[2 * e] = pack_half2(a.x, a.y);
-            hi[2 * e + 1] = pack_half2(b.x, b.y);
-            if constexpr (SPLIT) {
-              const __half2 ha = *reinterpret_cast<const __half2*>(&hi[2 * e]);
-              const __half2 hb = *reinterpret_cast<const __half2*>(&hi[2 * e + 1]);
-              lo[2 * e] = pack_half2(a.x - __low2float(ha), a.y - __high2float(ha));
-              lo[2 * e + 1] = pack_half2(b.x - __low2float(hb), b.y - __high2float(hb));
+          for (int k = 0; k < 4; ++k) {
+            const float2 is = make_float2(isc[k], isc[k]), nm = make_float2(-m[k], -m[k]);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float2 a = fma2(u[k][j], is, nm);
+              a = make_float2(ex2(a.x), ex2(a.y));
+              sum = add2(sum, a);
+              a = mul2(a, nv2[4 * j]);
+              const uint32_t h = pack_half2(a.x, a.y);
+              hi[k >> 1][2 * j + (k & 1)] = h;
+              if constexpr (SPLIT) {
+                const __half2 hh = *reinterpret_cast<const __half2*>(&h);
+                lo[k >> 1][2 * j + (k & 1)] =
+                    pack_half2(a.x - __low2float(hh), a.y - __high2float(hh));
+              }
             }
+            l[k] += sum.x + sum.y;
           }
-          tmem_st16(ts + 32 * c, hi);
-          if constexpr (SPLIT) tmem_st16(ts + 32 * c + 16, lo);
+          tmem_st_frag(ts + 32 * c, hi[0]);
+          tmem_st_frag(ts + (16u << 16) + 32 * c, hi[1]);
+          if constexpr (SPLIT) {
+            tmem_st_frag(ts + 32 * c + 16, lo[0]);
+            tmem_st_frag(ts + (16u << 16) + 32 * c + 16, lo[1]);
+          }
         }
-        l += (l0.x + l0.y) + (l1.x + l1.y);
         tmem_wait_st();
         tc_fence_before();
       }
@@ -1280,17 +1326,26 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
       ++segs;
       if (active) {
         tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // a row's sum is spread over four lanes
+          l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+          l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+        }
+        const float mr = by_row(m), lr = by_row(l);
+        const int row = 32 * wq + lane;
+        const size_t at = (size_t)(s * d.sub + row);
+        float* const rec_o = d.o + at * kHeadDim;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
           tmem_ld32(to + 32 * c, o);
-          tmem_wait_ld();
-          if (valid) {
+          tmem_wait_ld32(o);
+          if (row < rows) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) st_global_v8(rec_o + 32 * c + e, o + e);
           }
         }
-        if (valid) *rec_ml = make_float2(m, l);
+        if (row < rows) d.ml[at] = make_float2(mr, lr);
         tc_fence_before();
       }
       __syncwarp();
