@@ -24,7 +24,7 @@ __constant__ float c_rthr[KVQ_CB_N_THR] = KVQ_CB_THR;
 struct RaggedItem {
   int b, p_lo, n;
   int64_t row;
-  int64_t pos;  // cache position of the first token
+  int64_t pos;  // cache position of the first token (pre-RoPE keys only)
   uint8_t* rec;  // the tile's records (head 0); null: nothing to do
   bool clear;    // the tile already holds tokens
   uint32_t flags;
@@ -34,7 +34,11 @@ __device__ __forceinline__ int64_t ragged_item0(const int32_t* cu, int b) {
   return ((int64_t)max(cu[b], 0) >> 5) + 2 * (int64_t)b;
 }
 
-__device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& p, int64_t item) {
+// Where a sequence's tiles begin follows from its first slot; its length is read
+// only for the positions of pre-RoPE keys, which leaves one CTA free to advance
+// it in the same launch otherwise (`advance`: the CTA of the item's KV head 0).
+__device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& p, int64_t item,
+                                                  bool advance) {
   RaggedItem it;
   it.rec = nullptr;
   it.flags = 0;
@@ -47,22 +51,36 @@ __device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& p, int64_t
   it.b = lo;
   const int64_t i = item - ragged_item0(p.cu, lo);
   const int64_t c0 = p.cu[lo], c1 = p.cu[lo + 1];
-  const int64_t len0 = p.len[lo];
   if (c1 <= c0 || i < 0) return it;
-  if (c0 < 0 || c1 > p.n_rows || len0 < 0 || len0 + (c1 - c0) > 0x7FFFFFFF) {
+  if (c0 < 0 || c1 > p.n_rows) {
     if (i == 0) it.flags = KVQ_FLAG_CAPACITY;
     return it;
   }
-  const int64_t tile = len0 / kTile + i;
-  const int64_t t_lo = max(len0, tile * kTile), t_hi = min(len0 + (c1 - c0), tile * kTile + kTile);
-  if (t_lo >= t_hi) return it;
-  it.p_lo = (int)(t_lo - tile * kTile);
-  it.n = (int)(t_hi - t_lo);
-  it.row = c0 + (t_lo - len0);
-  it.pos = t_lo;
-  it.clear = len0 > tile * kTile;
+  const int64_t first = p.slots[c0];
+  if (first == -1) return it;  // refused by the assignment
+  const int p0 = (int)(first & (kTile - 1));
+  const int64_t t_lo = i == 0 ? 0 : i * kTile - p0;  // the item's first token
+  if (t_lo >= c1 - c0) return it;
+  it.p_lo = i == 0 ? p0 : 0;
+  it.n = (int)min((int64_t)(kTile - it.p_lo), c1 - c0 - t_lo);
+  it.row = c0 + t_lo;
+  it.clear = it.p_lo > 0;
+  it.pos = 0;
+  if (p.rope) {
+    const int64_t len = p.len[lo];
+    it.pos = len + t_lo;
+    if (len < 0 || len + (c1 - c0) > 0x7FFFFFFF || (len & (kTile - 1)) != p0) {
+      if (i == 0) it.flags = (len & (kTile - 1)) != p0 ? KVQ_FLAG_BAD_PAGE : KVQ_FLAG_CAPACITY;
+      return it;
+    }
+  } else if (advance && i == 0 && threadIdx.x == 0) {
+    const int64_t len = p.len[lo], to = len + (c1 - c0);  // read by this thread alone
+    if ((len & (kTile - 1)) != p0) atomicOr(p.status, KVQ_FLAG_BAD_PAGE);
+    else if (len < 0 || to > 0x7FFFFFFF) atomicOr(p.status, KVQ_FLAG_CAPACITY);
+    else p.len[lo] = (int32_t)to;
+  }
   const int64_t slot = p.slots[it.row];
-  if (slot == -1) return it;  // refused by the assignment
+  if (slot == -1) return it;
   const int64_t page = slot >> p.span_shift;
   const int in_page = (int)(slot & (p.span - 1));
   if (slot < 0 || page >= p.n_pages || (in_page & (kTile - 1)) != it.p_lo ||
@@ -97,7 +115,7 @@ __global__ void __launch_bounds__(256, 4) append_ragged_kernel(RaggedParams p) {
                           2 * (int64_t)p.batch;
   for (int64_t item = blockIdx.x; item < n_items * p.n_kv; item += gridDim.x) {
     const int h = (int)(item % p.n_kv);
-    const RaggedItem it = ragged_item(p, item / p.n_kv);
+    const RaggedItem it = ragged_item(p, item / p.n_kv, DT >= 0 && h == 0);
     if (!it.rec) {
       if (it.flags && threadIdx.x == 0) atomicOr(p.status, it.flags);
       continue;
@@ -165,14 +183,15 @@ __global__ void __launch_bounds__(256, 4) append_ragged_kernel(RaggedParams p) {
   if (threadIdx.x == 0 && s_flags) atomicOr(p.status, s_flags);
 }
 
-// len += the sequence's tokens, unless the assignment refused them.
+// len += the sequence's tokens, unless the assignment refused them (pre-RoPE
+// keys: every CTA of the append reads the lengths).
 __global__ void ragged_len_kernel(RaggedParams p) {
   grid_dep_wait();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= p.batch) return;
   const int64_t c0 = p.cu[b], c1 = p.cu[b + 1], len = p.len[b];
   if (c1 <= c0 || c0 < 0 || c1 > p.n_rows || len < 0 || len + (c1 - c0) > 0x7FFFFFFF) return;
-  if (p.slots[c0] != -1) p.len[b] = (int32_t)(len + (c1 - c0));
+  if (p.slots[c0] != -1 && ((p.slots[c0] ^ len) & (kTile - 1)) == 0) p.len[b] = (int32_t)(len + (c1 - c0));
 }
 
 template <int BV>
@@ -204,7 +223,7 @@ cudaError_t launch_append_ragged(const RaggedParams& p, int bits_v, cudaStream_t
     default: return cudaErrorInvalidValue;
   }
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !p.rope) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.batch + 255) / 256));
   cfg.blockDim = dim3(256);

@@ -477,23 +477,49 @@ def decode_attn_window(cfg, plan_ptrs, cache_ptrs, lens, win_ptrs, wlens, R, max
 
 
 # ------------------------------------------ page bookkeeping, ragged batches
-def _need(t, name, dtype, *shape):
+class _Dtypes(dict):
+    """torch dtype -> type code; anything else is refused."""
+
+    def __missing__(self, dtype):
+        import torch
+        if not self:
+            self.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+            if dtype in self:
+                return self[dtype]
+        raise KVQError(ERR_ARG, f"dtype {dtype}: bfloat16, float16 or float32")
+
+
+_DTYPES = _Dtypes()
+
+
+def _stream_of(t):
+    """The current stream of the tensor's device, which must be the current
+    device: the library launches there."""
+    import torch
+    i = t.get_device()
+    if i != torch.cuda.current_device():
+        raise KVQError(ERR_ARG, f"tensors on device {i}, current device "
+                                f"{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(i)
+
+
+def _need(t, name, dtype, shape):
     """Refuse a tensor that is not a contiguous device array of this type and
-    shape (None: any size): the library only sees its address."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.dim() != len(shape) or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise KVQError(ERR_ARG, f"{name}: contiguous {dtype} device tensor of shape {shape}, not "
-                                f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    shape: the library only sees its address. (One line of tests: the smallest
+    calls are bound by the host.)"""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise KVQError(ERR_ARG, f"{name}: contiguous {dtype} device tensor of shape "
+                                f"{tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def make_page_state(table, held, free_ids, free_ring, page_tiles):
     """kvq_page_state over device tensors: table int32 [batch, max_pages],
     held int32 [batch], free_ids int32 [n_pages], free_ring int64 [2]."""
     import torch
-    _need(table, "table", torch.int32, None, None)
-    _need(held, "held", torch.int32, table.shape[0])
-    _need(free_ids, "free_ids", torch.int32, None)
-    _need(free_ring, "free_ring", torch.int64, 2)
+    _need(table, "table", torch.int32, (table.shape[0], table.shape[-1]))
+    _need(held, "held", torch.int32, table.shape[:1])
+    _need(free_ids, "free_ids", torch.int32, free_ids.shape[:1])
+    _need(free_ring, "free_ring", torch.int64, (2,))
     return PageState(table.data_ptr(), held.data_ptr(), free_ids.data_ptr(), free_ring.data_ptr(),
                      free_ids.shape[0], page_tiles, table.shape[1])
 
@@ -507,17 +533,20 @@ def pages_assign(state, lens, n_new, cu, slots, pos, ws, status):
     Fills cu int32 [batch + 1], slots int64 [n_slots], pos int32 [n_slots] (or
     None) and moves pages between the rows and the free ring."""
     import torch
-    batch = lens.shape[0]
-    _need(lens, "lens", torch.int32, batch)
-    _need(n_new, "n_new", torch.int32, batch)
-    _need(cu, "cu", torch.int32, batch + 1)
-    _need(slots, "slots", torch.int64, None)
+    i32 = torch.int32
+    batch, n_slots = lens.shape[0], slots.shape[0]
+    _need(lens, "lens", i32, (batch,))
+    _need(n_new, "n_new", i32, (batch,))
+    _need(cu, "cu", i32, (batch + 1,))
+    _need(slots, "slots", torch.int64, (n_slots,))
     if pos is not None:
-        _need(pos, "pos", torch.int32, slots.shape[0])
-    _check(lib().kvq_pages_assign(ctypes.byref(state), lens.data_ptr(), n_new.data_ptr(), batch,
-                                  slots.shape[0], cu.data_ptr(), slots.data_ptr(), _ptr(pos),
-                                  ws.data_ptr(), ws.numel() * ws.element_size(),
-                                  status.data_ptr(), _stream()))
+        _need(pos, "pos", i32, (n_slots,))
+        pos = pos.data_ptr()
+    rc = lib().kvq_pages_assign(state, lens.data_ptr(), n_new.data_ptr(), batch, n_slots,
+                                cu.data_ptr(), slots.data_ptr(), pos, ws.data_ptr(), ws.nbytes,
+                                status.data_ptr(), _stream_of(lens))
+    if rc:
+        _check(rc)
 
 
 def paged_append_ragged(cfg, plan_ptrs, k, v, cu, slots, pool, n_pages, page_tiles, lens, status,
@@ -526,20 +555,24 @@ def paged_append_ragged(cfg, plan_ptrs, k, v, cu, slots, pool, n_pages, page_til
     of pages_assign (rope_base > 1: pre-RoPE keys) and advance lens."""
     import torch
     batch, n_rows = lens.shape[0], k.shape[0]
-    _need(k, "k", k.dtype, None, cfg.n_kv_heads, 128)
-    _need(v, "v", k.dtype, n_rows, cfg.n_kv_heads, 128)
-    _need(cu, "cu", torch.int32, batch + 1)
-    _need(slots, "slots", torch.int64, None)
-    _need(lens, "lens", torch.int32, batch)
-    if slots.shape[0] < n_rows or pool.numel() * pool.element_size() < \
-            n_pages * page_bytes(cfg, page_tiles):
+    rows = (n_rows, cfg.n_kv_heads, 128)
+    _need(k, "k", k.dtype, rows)
+    _need(v, "v", k.dtype, rows)
+    _need(cu, "cu", torch.int32, (batch + 1,))
+    _need(slots, "slots", torch.int64, slots.shape[:1])
+    _need(lens, "lens", torch.int32, (batch,))
+    # a page holds page_tiles records of 512 (bits_k + bits_v) + 128 bytes per KV head
+    if slots.shape[0] < n_rows or pool.nbytes < \
+            n_pages * page_tiles * cfg.n_kv_heads * (512 * (cfg.bits_k + cfg.bits_v) + 128):
         raise KVQError(ERR_ARG, f"{slots.shape[0]} slots for {n_rows} rows, pool of "
-                                f"{pool.numel() * pool.element_size()} bytes")
-    _check(lib().kvq_paged_append_ragged(ctypes.byref(cfg), plan_ptrs.data_ptr(), k.data_ptr(),
-                                         v.data_ptr(), _dtype_code(k), n_rows, cu.data_ptr(),
-                                         slots.data_ptr(), batch, pool.data_ptr(), n_pages,
-                                         page_tiles, lens.data_ptr(), float(rope_base),
-                                         status.data_ptr(), _stream()))
+                                f"{pool.nbytes} bytes")
+    rc = lib().kvq_paged_append_ragged(cfg, plan_ptrs.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                       _DTYPES[k.dtype], n_rows, cu.data_ptr(), slots.data_ptr(),
+                                       batch, pool.data_ptr(), n_pages, page_tiles,
+                                       lens.data_ptr(), rope_base, status.data_ptr(),
+                                       _stream_of(lens))
+    if rc:
+        _check(rc)
 
 
 # ------------------------------------------------------------ shared prefixes
@@ -551,11 +584,12 @@ def prefix_decode_workspace_bytes(cfg, batch, n_q_heads, n_prefixes) -> int:
 def _prefix_args(prefix_lens, group_start, lens, q, out):
     import torch
     batch, n_prefixes = lens.shape[0], prefix_lens.shape[0]
-    _need(prefix_lens, "prefix_lens", torch.int32, n_prefixes)
-    _need(group_start, "group_start", torch.int32, n_prefixes + 1)
-    _need(lens, "lens", torch.int32, batch)
-    _need(q, "q", q.dtype, batch, None, 128)
-    _need(out, "out", out.dtype, batch, q.shape[1], 128)
+    rows = (batch, q.shape[1], 128)
+    _need(prefix_lens, "prefix_lens", torch.int32, (n_prefixes,))
+    _need(group_start, "group_start", torch.int32, (n_prefixes + 1,))
+    _need(lens, "lens", torch.int32, (batch,))
+    _need(q, "q", q.dtype, rows)
+    _need(out, "out", out.dtype, rows)
     return batch, n_prefixes
 
 
@@ -565,12 +599,14 @@ def prefix_decode_attn(cfg, plan_ptrs, prefix_ptrs, prefix_lens, group_start, ma
     group's shared prefix cache (sequences group_start[g] .. group_start[g + 1]
     - 1 share prefix g) and each sequence's own cache."""
     batch, n_prefixes = _prefix_args(prefix_lens, group_start, lens, q, out)
-    _check(lib().kvq_prefix_decode_attn(
-        ctypes.byref(cfg), plan_ptrs.data_ptr(), prefix_ptrs.data_ptr(), prefix_lens.data_ptr(),
+    rc = lib().kvq_prefix_decode_attn(
+        cfg, plan_ptrs.data_ptr(), prefix_ptrs.data_ptr(), prefix_lens.data_ptr(),
         group_start.data_ptr(), n_prefixes, max_prefix_len, cache_ptrs.data_ptr(),
-        lens.data_ptr(), batch, max_len, q.data_ptr(), _dtype_code(q), q.shape[1],
-        out.data_ptr(), _dtype_code(out), ws.data_ptr(), ws.numel() * ws.element_size(),
-        status.data_ptr(), _stream()))
+        lens.data_ptr(), batch, max_len, q.data_ptr(), _DTYPES[q.dtype], q.shape[1],
+        out.data_ptr(), _DTYPES[out.dtype], ws.data_ptr(), ws.nbytes, status.data_ptr(),
+        _stream_of(q))
+    if rc:
+        _check(rc)
 
 
 def paged_prefix_decode_attn(cfg, plan_ptrs, prefix_pages, prefix_lens, group_start,
@@ -578,9 +614,10 @@ def paged_prefix_decode_attn(cfg, plan_ptrs, prefix_pages, prefix_lens, group_st
     """prefix_decode_attn over paged caches (the prefixes' block-table rows in
     prefix_pages, the sequences' in pages)."""
     batch, n_prefixes = _prefix_args(prefix_lens, group_start, lens, q, out)
-    _check(lib().kvq_paged_prefix_decode_attn(
-        ctypes.byref(cfg), plan_ptrs.data_ptr(), ctypes.byref(prefix_pages),
-        prefix_lens.data_ptr(), group_start.data_ptr(), n_prefixes, max_prefix_len,
-        ctypes.byref(pages), lens.data_ptr(), batch, max_len, q.data_ptr(), _dtype_code(q),
-        q.shape[1], out.data_ptr(), _dtype_code(out), ws.data_ptr(),
-        ws.numel() * ws.element_size(), status.data_ptr(), _stream()))
+    rc = lib().kvq_paged_prefix_decode_attn(
+        cfg, plan_ptrs.data_ptr(), prefix_pages, prefix_lens.data_ptr(), group_start.data_ptr(),
+        n_prefixes, max_prefix_len, pages, lens.data_ptr(), batch, max_len, q.data_ptr(),
+        _DTYPES[q.dtype], q.shape[1], out.data_ptr(), _DTYPES[out.dtype], ws.data_ptr(),
+        ws.nbytes, status.data_ptr(), _stream_of(q))
+    if rc:
+        _check(rc)

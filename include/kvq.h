@@ -693,12 +693,14 @@ KVQ_API int kvq_pages_assign(const kvq_page_state* state, const int32_t* len_dev
  * part-filled tiles are those of kvq_quantize_append. Then len_dev[b] += its rows.
  * A sequence whose first slot is -1 was refused: nothing is stored, its length
  * stays (a tile whose slot is -1 is skipped). A slot outside the pool, or slots
- * of a tile that do not follow len, flag BAD_PAGE and skip the tile; cu outside
- * 0..n_rows or a negative or overflowing length flags CAPACITY and skips the
- * sequence. Different sequences' slots must not lie in one tile.
+ * of a tile that are not consecutive, flag BAD_PAGE and skip the tile; cu outside
+ * 0..n_rows flags CAPACITY and skips the sequence. A first slot whose position in
+ * its tile is not len's flags BAD_PAGE, a negative or overflowing length CAPACITY:
+ * the length then stays, and the sequence's rows may or may not be stored (at
+ * their slots). Different sequences' slots must not lie in one tile.
  * pool, n_pages, page_tiles: as in kvq_pages. n_rows 0..2^31 - 1 (0: no work).
  * rope_base = 0: post-RoPE keys; rope_base > 1: pre-RoPE keys, each rotated to
- * its position as by kvq_quantize_append_rope. Two launches.
+ * its position as by kvq_quantize_append_rope. One launch (pre-RoPE keys: two).
  */
 KVQ_API int kvq_paged_append_ragged(const kvq_cfg* cfg, const void* const* plans_dev,
                                     const void* k_dev, const void* v_dev, int dtype,
