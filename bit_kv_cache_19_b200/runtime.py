@@ -173,6 +173,22 @@ class PackedLayer:
         kvq.combine_partials(self.cfg, self.plan_ptrs, recs, out)
         return out
 
+    def decode_prefix(self, q, prefix, group_start, out=None, ws=None, max_len=None,
+                      max_prefix_len=None):
+        """q [batch, n_q, 128] over shared prefixes, then each sequence's own
+        tokens: sequences group_start[g] .. group_start[g + 1] - 1 (int32, device)
+        share sequence g of ``prefix``, another PackedLayer with the same plans.
+        out: q's type unless given (bf16, fp16 or fp32)."""
+        if out is None:
+            out = torch.empty_like(q)
+        if ws is None:
+            ws = prefix_workspace(self.cfg, self.batch, q.shape[1], prefix.batch, self.device)
+        kvq.prefix_decode_attn(
+            self.cfg, self.plan_ptrs, prefix.cache_ptrs, prefix.lens, group_start,
+            prefix.cap if max_prefix_len is None else max_prefix_len, self.cache_ptrs, self.lens,
+            self.cap if max_len is None else max_len, q, out, ws, self.status)
+        return out
+
     def decode_sharded(self, q, group=None, max_len=None):
         """Context-sharded decode: this rank's caches hold one token range of
         each sequence (ranks in sequence order); one all-gather of records."""
@@ -193,6 +209,12 @@ class PackedLayer:
 
     def flags(self) -> int:
         return int(self.status.item()) & 0xFFFFFFFF
+
+
+def prefix_workspace(cfg, batch: int, n_q: int, n_prefixes: int, device="cuda"):
+    """Workspace of decode_prefix (no initial value)."""
+    return torch.empty(kvq.prefix_decode_workspace_bytes(cfg, batch, n_q, n_prefixes),
+                       dtype=torch.uint8, device=device)
 
 
 def sharded_decode(partial, combine, group=None):
@@ -258,15 +280,60 @@ class PageAllocator:
         self.n_held[seq] = 0
 
 
+class DevicePageAllocator:
+    """Page bookkeeping on the GPU (kvq_pages_assign): the block table, the pages
+    each sequence holds and the ring of free page ids live on the device, so a
+    serving step assigns pages without the host and can be captured in a graph.
+    Layers of one model that grow alike can share one allocator."""
+
+    def __init__(self, n_pages: int, page_tiles: int, batch: int, max_pages: int,
+                 device="cuda"):
+        self.n_pages = n_pages
+        self.page_tiles = page_tiles
+        self.batch = batch
+        self.max_pages = max_pages
+        self.device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.table = torch.full((batch, max_pages), -1, **i32)
+        self.held = torch.zeros(batch, **i32)
+        self.free_ids = torch.arange(n_pages, **i32)
+        self.free_ring = torch.tensor([0, n_pages], dtype=torch.int64, device=self.device)
+        self.state = kvq.make_page_state(self.table, self.held, self.free_ids, self.free_ring,
+                                         page_tiles)
+        self.status = torch.zeros(1, **i32)
+        self.ws = torch.empty(kvq.pages_assign_workspace_bytes(batch), dtype=torch.uint8,
+                              device=self.device)
+
+    def assign(self, lens, n_new, n_slots: int = None, cu=None, slots=None, pos=None):
+        """Pages for n_new int32 [batch] tokens after lengths lens (device):
+        (cu int32 [batch + 1], slots int64 [n_slots], pos int32 [n_slots]) of the
+        step's packed tokens. Pages past a sequence's new length are returned
+        (lens = n_new = 0 releases a sequence). n_slots: the most tokens of the
+        step (needed unless slots is given)."""
+        if slots is None:
+            slots = torch.empty(n_slots, dtype=torch.int64, device=self.device)
+        if pos is None:
+            pos = torch.empty(slots.shape[0], dtype=torch.int32, device=self.device)
+        if cu is None:
+            cu = torch.empty(self.batch + 1, dtype=torch.int32, device=self.device)
+        kvq.pages_assign(self.state, lens, n_new, cu, slots, pos, self.ws, self.status)
+        return cu, slots, pos
+
+    def flags(self) -> int:
+        return int(self.status.item()) & 0xFFFFFFFF
+
+
 class PagedLayer:
     """One layer's packed caches for a batch of sequences in pages of a shared
     pool: the pool, the block table (device) and a host-side page allocator.
     Pages are handed out in order from a free list as sequences grow
     (``reserve``) and returned by ``release``; the kernels only follow the
-    block table."""
+    block table. With ``pages`` (a DevicePageAllocator, which several layers may
+    share) the block table is the allocator's and pages are assigned on the
+    GPU: ``assign`` before each ``append_ragged``."""
 
     def __init__(self, cfg, batch: int, n_pages: int, page_tiles: int, max_pages: int,
-                 device="cuda", layer: int = 0):
+                 device="cuda", layer: int = 0, pages: DevicePageAllocator = None):
         self.cfg = cfg
         self.batch = batch
         self.layer = layer
@@ -277,8 +344,16 @@ class PagedLayer:
         if nb == 0:
             raise ValueError(f"page_tiles {page_tiles}: a power of two, 1..2^20")
         self.pool = torch.zeros(n_pages * nb, dtype=torch.uint8, device=self.device)
-        self.alloc = PageAllocator(n_pages, page_tiles, batch, max_pages)
-        self.table = torch.from_numpy(self.alloc.table.copy()).to(self.device)
+        self.dev_pages = pages
+        if pages is None:
+            self.alloc = PageAllocator(n_pages, page_tiles, batch, max_pages)
+            self.table = torch.from_numpy(self.alloc.table.copy()).to(self.device)
+        else:
+            if (pages.n_pages, pages.page_tiles, pages.batch, pages.max_pages) != (
+                    n_pages, page_tiles, batch, max_pages):
+                raise ValueError("the allocator's pages, batch or rows are not the layer's")
+            self.alloc = None
+            self.table = pages.table
         self.pages = kvq.make_pages(self.pool, self.table, n_pages, page_tiles)
         self.plans = torch.zeros(cfg.n_kv_heads * kvq.PLAN_BYTES, dtype=torch.uint8,
                                  device=self.device)
@@ -289,25 +364,60 @@ class PagedLayer:
 
     @property
     def table_host(self):
-        return self.alloc.table
+        return self.table.cpu().numpy() if self.alloc is None else self.alloc.table
 
     @property
     def cap(self) -> int:
-        return self.alloc.table.shape[1] * self.page_tiles * 32
+        return self.table.shape[1] * self.page_tiles * 32
 
     # ---------------------------------------------------------- pages
     def reserve(self, seq: int, n_tokens: int, order=None):
         """Pages for the first n_tokens tokens of sequence seq; uploads the table."""
+        self._host_pages()
         self.alloc.reserve(seq, n_tokens, order)
         self.table.copy_(torch.from_numpy(self.alloc.table))
 
     def release(self, seq: int):
         """Return a sequence's pages to the free list and empty it."""
+        self._host_pages()
         self.alloc.release(seq)
         self.table.copy_(torch.from_numpy(self.alloc.table))
         self.lens[seq] = 0
 
+    def _host_pages(self):
+        if self.alloc is None:
+            raise RuntimeError("pages are assigned on the GPU (assign)")
+
+    def assign(self, n_new, n_slots: int = None, **buffers):
+        """DevicePageAllocator.assign for this layer's lengths: (cu, slots, pos).
+        To release a sequence, set its length (``lens``) and count to 0."""
+        if self.dev_pages is None:
+            raise RuntimeError("this layer's pages are assigned on the host (reserve)")
+        return self.dev_pages.assign(self.lens, n_new, n_slots, **buffers)
+
     # ---------------------------------------------------------- calls
+    def append_ragged(self, k, v, cu, slots, rope_base=0.0):
+        """Packed rows k, v [n_rows, n_kv, 128] of all sequences into the slots
+        of an assignment (rope_base > 1: pre-RoPE keys); advances ``lens``."""
+        kvq.paged_append_ragged(self.cfg, self.plan_ptrs, k, v, cu, slots, self.pool,
+                                self.n_pages, self.page_tiles, self.lens, self.status, rope_base)
+
+    def decode_prefix(self, q, prefix, group_start, out=None, ws=None, max_len=None,
+                      max_prefix_len=None):
+        """q [batch, n_q, 128] over shared prefixes, then each sequence's own
+        tokens: sequences group_start[g] .. group_start[g + 1] - 1 (int32, device)
+        share row g of ``prefix``, another PagedLayer with the same plans. out:
+        q's type unless given (bf16, fp16 or fp32)."""
+        if out is None:
+            out = torch.empty_like(q)
+        if ws is None:
+            ws = prefix_workspace(self.cfg, self.batch, q.shape[1], prefix.batch, self.device)
+        kvq.paged_prefix_decode_attn(
+            self.cfg, self.plan_ptrs, prefix.pages, prefix.lens, group_start,
+            prefix.cap if max_prefix_len is None else max_prefix_len, self.pages, self.lens,
+            self.cap if max_len is None else max_len, q, out, ws, self.status)
+        return out
+
     def alloc_bits(self, k):
         """Plans from keys k [T, n_kv, 128] (device), as PackedLayer.alloc_bits."""
         self.plans_host, self.energy = kvq.alloc_bits(self.cfg, self.layer, k, self.plans,
