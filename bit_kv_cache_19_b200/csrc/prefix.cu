@@ -68,6 +68,7 @@ constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kPTop = 15.f, kPSet = 7.f;
 // cost of a segment's start and of one tile (shared: 256 rows; else <= 128)
 constexpr int kCostSeg = 3, kCostShared = 5, kCostAlt = 3;
+constexpr int kDescs = 4;  // segments in flight
 
 // ---------------------------------------------------------------- workspace
 struct PfxHead {
@@ -76,9 +77,12 @@ struct PfxHead {
   int64_t n_cuts;   // CTAs that get a piece of the cost line
   int64_t pad;
 };
-// First unit of a CTA's piece: a sequence (suffix) or a group, KV head, row tile.
-struct alignas(16) PfxFirst {
-  int32_t suffix, i, h, rt;
+// A unit of work: a row tile of a prefix (group g, first sequence b) and KV head,
+// or a sequence's own tokens (suffix; sequence b).
+struct alignas(16) Unit {
+  int64_t start, cost, idx;  // position and length on the cost line; number
+  int32_t suffix, shared;
+  int32_t g, b, h, rt, nrt, rows, len, tiles;
 };
 // Prefix rows of a sequence: unit of KV head 0 (-1: no prefix), row tiles per KV
 // head, first row in the group.
@@ -112,7 +116,7 @@ static PfxLayout pfx_layout(int batch, int n_q, int n_kv, int n_groups, int n_ct
   };
   w.head = take(sizeof(PfxHead));
   w.cuts = take((size_t)(n_ctas + 1) * 8);
-  w.first = take((size_t)n_ctas * sizeof(PfxFirst));
+  w.first = take((size_t)n_ctas * sizeof(Unit));
   w.row = take((size_t)batch * sizeof(PfxRow));
   w.unit_p = take(units * sizeof(PfxUnit));
   w.unit_s = take((size_t)batch * n_kv * sizeof(PfxUnit));
@@ -138,7 +142,7 @@ struct PrefixParams {
   int rows_unit;  // 256 or 128 rows per prefix unit
   PfxHead* head;
   int64_t* cuts;  // [n_ctas + 1] first position of each CTA's piece
-  PfxFirst* first;  // [n_ctas]
+  Unit* first;      // [n_ctas] first unit of each CTA's piece
   PfxRow* row;      // [batch]
   PfxUnit *unit_p, *unit_s;
   int32_t *gstart, *gunit;
@@ -182,6 +186,45 @@ __device__ __forceinline__ int tiles_before(int64_t x, int64_t start, int tiles,
   if (d >= (int64_t)tiles * (shared ? kCostShared : kCostAlt)) return tiles;
   const uint32_t e = (uint32_t)d;  // tiles < 2^24
   return (int)(shared ? (e + kCostShared - 1) / kCostShared : (e + kCostAlt - 1) / kCostAlt);
+}
+
+// Unit (h, rt) of group g: rows of the group in all, tiles and length of the
+// prefix, the group's position on the cost line and first unit number.
+__device__ __forceinline__ Unit make_prefix_unit(const PrefixParams& p, int g, int h, int rt,
+                                                 int b0, int rows, int len, int64_t gcost,
+                                                 int gunit) {
+  Unit u;
+  u.suffix = 0;
+  u.g = g;
+  u.b = b0;
+  u.h = h;
+  u.rt = rt;
+  u.len = len;
+  u.tiles = tiles_of(len);
+  const GroupCost c = group_cost(rows, u.tiles, p.rows_unit);
+  u.nrt = c.nrt;
+  u.rows = rt == c.nrt - 1 ? c.last : p.rows_unit;
+  u.shared = u.rows > 128;
+  u.start = gcost + h * c.block + rt * c.full;
+  u.cost = rt == c.nrt - 1 ? c.lastc : c.full;
+  u.idx = gunit + h * c.nrt + rt;
+  return u;
+}
+__device__ __forceinline__ Unit make_suffix_unit(const PrefixParams& p, int b, int h, int len,
+                                                 int64_t scost) {
+  Unit u;
+  u.suffix = 1;
+  u.shared = 0;
+  u.g = u.rt = u.nrt = 0;
+  u.b = b;
+  u.h = h;
+  u.rows = p.G;
+  u.len = len;
+  u.tiles = tiles_of(len);
+  u.cost = u.tiles > 0 ? kCostSeg + (int64_t)u.tiles * kCostAlt : 0;
+  u.start = scost + h * u.cost;
+  u.idx = (int64_t)b * p.a.n_kv + h;
+  return u;
 }
 
 // ---------------------------------------------------------------------- prep
@@ -330,24 +373,24 @@ __device__ __forceinline__ void prep_schedule(const PrefixParams& p, PrepSmem& s
     const int64_t x = c < pieces ? base * c / pieces : base;
     p.cuts[c] = x;
     if (c >= p.n_ctas || x >= base) continue;
-    PfxFirst f;
-    f.suffix = x >= suffix0;
-    f.rt = 0;
-    if (f.suffix) {
-      f.i = last_at(p.scost, p.a.batch, x);
-      const int64_t cost =
-          seq_cost(tiles_of(clamp_len(p.a.len[f.i], p.a.max_len)), p.a.n_kv) / p.a.n_kv;
-      f.h = (int)((x - p.scost[f.i]) / cost);
+    if (x >= suffix0) {
+      const int i = last_at(p.scost, p.a.batch, x);
+      Unit u = make_suffix_unit(p, i, 0, clamp_len(p.a.len[i], p.a.max_len), p.scost[i]);
+      const int h = (int)((x - u.start) / u.cost);
+      u.h = h;
+      u.start += h * u.cost;
+      u.idx += h;
+      p.first[c] = u;
     } else {
-      f.i = last_at(sm.gcost, n, x);
-      const int rows = (sm.gstart[f.i + 1] - sm.gstart[f.i]) * p.G;
-      const GroupCost gc =
-          group_cost(rows, tiles_of(clamp_len(p.a.pre_len[f.i], p.a.max_pre)), p.rows_unit);
-      const int64_t d = x - sm.gcost[f.i];
-      f.h = (int)(d / gc.block);
-      f.rt = (int)min((d - f.h * gc.block) / gc.full, (int64_t)gc.nrt - 1);
+      const int i = last_at(sm.gcost, n, x);
+      const int rows = (sm.gstart[i + 1] - sm.gstart[i]) * p.G;
+      const int len = clamp_len(p.a.pre_len[i], p.a.max_pre);
+      const GroupCost gc = group_cost(rows, tiles_of(len), p.rows_unit);
+      const int64_t d = x - sm.gcost[i];
+      const int h = (int)(d / gc.block);
+      const int rt = (int)min((d - h * gc.block) / gc.full, (int64_t)gc.nrt - 1);
+      p.first[c] = make_prefix_unit(p, i, h, rt, sm.gstart[i], rows, len, sm.gcost[i], sm.gunit[i]);
     }
-    p.first[c] = f;
   }
   if (flags) atomicOr(p.a.status, flags);
 }
@@ -502,16 +545,18 @@ struct alignas(16) Desc {  // one segment: a run of tiles of one unit
   const float* isc;
   unsigned long long base[32];  // page bases of the first 32 records (0: refused)
   int suffix, row;              // cache map and its row
+  int par;  // stream of the segment's first item
   int stop, shared, rows, tiles, tile0, len, b0, row0, h, qslot, sub;
 };
 
 struct alignas(128) MainSmem {
   uint8_t lut[KVQ_LUT_BYTES];
-  Desc desc[2];
+  Desc desc[kDescs];
   alignas(16) float nk[kNormSlots][kTok];
   alignas(16) float nv[kNormSlots][kTok];
   int lg[kNormSlots][4];  // per record: the value norms are below 2^lg
-  unsigned long long desc_full[2], desc_empty[2], ring_full[kMaxRing], ring_empty[kMaxRing];
+  unsigned long long desc_ready[kDescs], desc_full[kDescs], desc_empty[kDescs];
+  unsigned long long ring_full[kMaxRing], ring_empty[kMaxRing];
   unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full, v_empty;
   unsigned long long s_full[2], p_ready[2], o_full[2], o_free[2], lut_full, drain;
   uint32_t tmem;
@@ -551,49 +596,6 @@ struct RingPos {
     }
   }
 };
-
-// Unit of work during the walk along the cost line (warp-uniform).
-struct Unit {
-  bool suffix, shared;
-  int g, b, h, rt;    // prefix: group, KV head, row tile; suffix: sequence, KV head
-  int nrt, rows, len, tiles;
-  int64_t start, cost, idx;
-};
-
-__device__ __forceinline__ Unit prefix_unit(const PrefixParams& p, int g, int h, int rt) {
-  Unit u;
-  const int b0 = p.gstart[g], rows = (p.gstart[g + 1] - b0) * p.G;
-  u.suffix = false;
-  u.g = g;
-  u.b = b0;
-  u.h = h;
-  u.rt = rt;
-  u.len = clamp_len(p.a.pre_len[g], p.a.max_pre);
-  u.tiles = tiles_of(u.len);
-  const GroupCost c = group_cost(rows, u.tiles, p.rows_unit);
-  u.nrt = c.nrt;
-  u.rows = rt == c.nrt - 1 ? c.last : p.rows_unit;
-  u.shared = u.rows > 128;
-  u.start = p.gcost[g] + h * c.block + rt * c.full;
-  u.cost = rt == c.nrt - 1 ? c.lastc : c.full;
-  u.idx = p.gunit[g] + h * c.nrt + rt;
-  return u;
-}
-__device__ __forceinline__ Unit suffix_unit(const PrefixParams& p, int b, int h) {
-  Unit u;
-  u.suffix = true;
-  u.shared = false;
-  u.g = u.rt = u.nrt = 0;
-  u.b = b;
-  u.h = h;
-  u.rows = p.G;
-  u.len = clamp_len(p.a.len[b], p.a.max_len);
-  u.tiles = tiles_of(u.len);
-  u.cost = u.tiles > 0 ? kCostSeg + (int64_t)u.tiles * kCostAlt : 0;
-  u.start = p.scost[b] + h * u.cost;
-  u.idx = (int64_t)b * p.a.n_kv + h;
-  return u;
-}
 
 // Largest i in [0, n) with a[i] <= x, by a warp (a ascending, a[0] <= x).
 __device__ __forceinline__ int warp_last_le(const int64_t* a, int n, int64_t x, int lane) {
@@ -786,6 +788,24 @@ __device__ __forceinline__ void unpack_values(const uint8_t* lut, const uint8_t*
 
 // ---- the roles of the main kernel
 
+// The unit with a cost that follows u on the cost line (there is one).
+__device__ __forceinline__ Unit next_unit(const PrefixParams& p, const Unit& u, int64_t suffix0,
+                                          int lane) {
+  const int64_t x = u.start + u.cost;
+  int i = u.suffix ? u.b : u.g, h = u.h, rt = 0;
+  const bool suffix = x >= suffix0;
+  if (!u.suffix && !suffix && u.rt + 1 < u.nrt) {
+    rt = u.rt + 1;
+  } else if (u.suffix != (int)suffix || ++h == p.a.n_kv) {
+    h = 0;
+    i = warp_last_le(suffix ? p.scost : p.gcost, suffix ? p.a.batch : p.a.n_groups, x, lane);
+  }
+  if (suffix)
+    return make_suffix_unit(p, i, h, clamp_len(p.a.len[i], p.a.max_len), p.scost[i]);
+  return make_prefix_unit(p, i, h, rt, p.gstart[i], (p.gstart[i + 1] - p.gstart[i]) * p.G,
+                          clamp_len(p.a.pre_len[i], p.a.max_pre), p.gcost[i], p.gunit[i]);
+}
+
 // Walks the CTA's piece of the cost line: one descriptor, plan and query image
 // per segment, ahead of the other roles.
 template <bool SPLIT>
@@ -794,42 +814,30 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
   const int64_t suffix0 = p.head->suffix0;
   const int n_cuts = (int)p.head->n_cuts;
   const int64_t x0 = p.cuts[blockIdx.x], x1 = p.cuts[blockIdx.x + 1];
-  PfxFirst f = p.first[blockIdx.x];  // of a CTA without a piece: not used
+  Unit u = p.first[blockIdx.x];  // of a CTA without a piece: not used
   uint32_t seg = 0;                // segments
+  uint32_t items = 0;              // tiles of one stream so far
   uint32_t quse[2] = {0u, 0u};     // segments that used each query slot
   int qnext = 0;
   bool ok = true;
   bool more = x0 < x1;
 #pragma unroll 1
   while (ok && more) {
-    const Unit u = f.suffix ? suffix_unit(p, f.i, f.h) : prefix_unit(p, f.i, f.h, f.rt);
     const int t0 = tiles_before(x0, u.start, u.tiles, u.shared);
     const int t1 = tiles_before(x1, u.start, u.tiles, u.shared);
-    const int row = f.i, n_rec = (u.len + kTile - 1) / kTile;
+    more = u.start + u.cost < x1;
+    if (t0 >= t1) {
+      if (more) u = next_unit(p, u, suffix0, lane);
+      continue;
+    }
+    const int row = u.suffix ? u.b : u.g, n_rec = (u.len + kTile - 1) / kTile;
     const Plan* const plan = p.a.plans[u.b] + u.h;
     unsigned long long base = 0;
-    if (t0 < t1 && 4 * t0 + lane < n_rec)
+    if (4 * t0 + lane < n_rec)
       base = (unsigned long long)(uintptr_t)page_base(u.suffix ? p.a.own : p.a.pre, row,
                                                       4 * t0 + lane);
-    // the next unit with a cost, if this CTA's piece goes on
-    const int64_t x = u.start + u.cost;
-    more = x < x1;
-    if (more) {
-      const bool cross = !f.suffix && x >= suffix0;
-      if (f.suffix) {
-        if (++f.h == p.a.n_kv) f.i = warp_last_le(p.scost, p.a.batch, x, lane);
-      } else if (cross) {
-        f.i = warp_last_le(p.scost, p.a.batch, x, lane);
-      } else if (++f.rt == u.nrt) {
-        f.rt = 0;
-        if (++f.h == p.a.n_kv) f.i = warp_last_le(p.gcost, p.a.n_groups, x, lane);
-      }
-      if (cross || f.h == p.a.n_kv) f.h = f.rt = 0;
-      f.suffix = x >= suffix0;
-    }
-    if (t0 >= t1) continue;
-    const uint32_t ds = seg & 1;
-    ok = wait_warp(sm, &sm.desc_empty[ds], ((seg >> 1) & 1) ^ 1);
+    const uint32_t ds = seg % kDescs;
+    ok = wait_warp(sm, &sm.desc_empty[ds], ((seg / kDescs) & 1) ^ 1);
     if (!ok) break;
     const bool both = u.shared || SPLIT;
     const int qs = both ? 0 : qnext;
@@ -854,11 +862,14 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
       d.h = u.h;
       d.qslot = qs;
       d.sub = u.suffix ? p.G : 128;
+      d.par = (int)(items & 1);
+      mbar_arrive(&sm.desc_ready[ds]);
       mbar_expect_tx(&sm.desc_full[ds], KVQ_PLAN_BYTES);
       bulk_g2s(&d.plan, plan, KVQ_PLAN_BYTES, &sm.desc_full[ds]);
     }
     __syncwarp();
     ++seg;
+    items += (t1 - t0) << (u.shared ? 1 : 0);
 #pragma unroll 1
     for (int i = 0; i < (both ? 2 : 1); ++i) {
       const int s = qs + i;
@@ -888,20 +899,22 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
         (u.suffix ? p.unit_s : p.unit_p)[u.idx] =
             PfxUnit{u.start, u.tiles, u.shared, (int)blockIdx.x, c1, {0, 0}};
     }
+    if (more) u = next_unit(p, u, suffix0, lane);
   }
   if (ok) {  // the end of the CTA's work
-    const uint32_t ds = seg & 1;
-    ok = wait_warp(sm, &sm.desc_empty[ds], ((seg >> 1) & 1) ^ 1);
+    const uint32_t ds = seg % kDescs;
+    ok = wait_warp(sm, &sm.desc_empty[ds], ((seg / kDescs) & 1) ^ 1);
     if (ok && lane == 0) {
       sm.desc[ds].stop = 1;
+      mbar_arrive(&sm.desc_ready[ds]);
       mbar_arrive(&sm.desc_full[ds]);
     }
   }
   if (!ok) {  // let the copies in flight land before the CTA ends
     if (quse[0]) (void)mbar_wait_bounded(&sm.q_full[0], (quse[0] - 1) & 1);
     if (quse[1]) (void)mbar_wait_bounded(&sm.q_full[1], (quse[1] - 1) & 1);
-    for (uint32_t i = 1; i <= 2 && i <= seg; ++i)
-      (void)mbar_wait_bounded(&sm.desc_full[(seg - i) & 1], ((seg - i) >> 1) & 1);
+    for (uint32_t i = 1; i <= kDescs && i <= seg; ++i)
+      (void)mbar_wait_bounded(&sm.desc_full[(seg - i) % kDescs], ((seg - i) / kDescs) & 1);
   }
 }
 
@@ -914,8 +927,8 @@ __device__ __forceinline__ void copy_role(const PrefixParams& p, MainSmem& sm, u
   uint32_t issued = 0;  // slots that copies have been issued to
   bool ok = true;
   for (uint32_t seg = 0; ok; ++seg) {
-    const uint32_t ds = seg & 1;
-    ok = wait_warp(sm, &sm.desc_full[ds], (seg >> 1) & 1);
+    const uint32_t ds = seg % kDescs;
+    ok = wait_warp(sm, &sm.desc_ready[ds], (seg / kDescs) & 1);
     const Desc& d = sm.desc[ds];
     if (!ok || d.stop) break;
     const int tiles = d.tiles, n_rec = (d.len + kTile - 1) / kTile, row = d.row, h = d.h;
@@ -981,8 +994,8 @@ __device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm,
   const uint32_t tbytes = p.tile_bytes;
   if (!wait_warp(sm, &sm.lut_full, 0)) return;
   for (;; ++seg) {
-    const uint32_t ds = seg & 1;
-    if (!wait_warp(sm, &sm.desc_full[ds], (seg >> 1) & 1)) return;
+    const uint32_t ds = seg % kDescs;
+    if (!wait_warp(sm, &sm.desc_full[ds], (seg / kDescs) & 1)) return;
     const Desc& d = sm.desc[ds];
     if (d.stop) return;
     const Plan& pl = d.plan;
@@ -1059,96 +1072,128 @@ __device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm,
 // D fp32, A and B fp16 K-major, M = N = 128.
 constexpr uint32_t kIdesc = (1u << 4) | (16u << 17) | (8u << 24);
 
+// A segment's items, in order (item = one stream's tile: of a shared segment the
+// two row tiles of each tile in turn, else its tiles).
+struct ItemCursor {
+  uint32_t seg, j, n, tile0;  // segment, next item, items, number of its first tile
+  bool shared;
+  __device__ __forceinline__ uint32_t tile() const { return tile0 + (shared ? j >> 1 : j); }
+  __device__ __forceinline__ bool first_use() const { return !shared || !(j & 1); }
+  __device__ __forceinline__ bool last_use() const { return !shared || (j & 1); }
+  __device__ __forceinline__ void load(const Desc& d) {
+    tile0 += shared ? n >> 1 : n;
+    shared = d.shared;
+    n = (uint32_t)d.tiles << (shared ? 1 : 0);
+    j = 0;
+  }
+};
+
+// Step k: P V of item k - 2, then Q K of item k, through all segments in one
+// sequence; item k belongs to stream k mod 2, so a stream starts a segment as soon
+// as it has finished its part of the one before.
 template <bool SPLIT>
 __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, const uint8_t* qbuf,
                          const uint8_t* kbuf, const uint8_t* vbuf, uint32_t tmem) {
   const bool elected = elect_one();
   // phases: bit s of quse (query slot s), items and segs (stream s)
-  uint32_t quse = 0, items = 0, segs = 0, tile_base = 0;
+  uint32_t quse = 0, items = 0, segs = 0;
   // low words of the operand descriptors (addresses in units of 16 bytes)
   const uint32_t qd = desc_lo(smem_addr(qbuf)), kd = desc_lo(smem_addr(kbuf)),
                  vd = desc_lo(smem_addr(vbuf));
   constexpr uint32_t kTileD = kTileBytes >> 4, kPanelD = kPanel >> 4;
-  for (uint32_t seg = 0;; ++seg) {
-    const uint32_t ds = seg & 1;
-    if (!wait_warp(sm, &sm.desc_full[ds], (seg >> 1) & 1)) return;
-    const Desc& d = sm.desc[ds];
-    if (d.stop) return;
-    const bool shared = d.shared;
-    const int tiles = d.tiles, n_items = shared ? 2 * tiles : tiles, q0 = d.qslot;
-    const uint32_t ksteps = (min(max(d.plan.n_ranks, 1), 64) + 7) / 8;
-    const bool both = shared || SPLIT;
+  ItemCursor q{0u, 0u, 0u, 0u, false}, v{0u, 0u, 0u, 0u, false};
+  uint32_t ksteps = 0;
+  int q0 = 0;
+  bool more = true;
 #pragma unroll 1
-    for (int i = q0; i < q0 + (both ? 2 : 1); ++i) {
-      if (!wait_warp(sm, &sm.q_full[i], quse >> i & 1)) return;
-      quse ^= 1u << i;
-    }
-    // step j: P V of item j - 2, then Q K of item j (item = a stream's tile;
-    // items alternate between the streams)
-#pragma unroll 1
-    for (int j = 0; j < n_items + 2; ++j) {
-      const int s = j & 1;
-      if (j >= 2) {
-        const int i = j - 2, t = shared ? i >> 1 : i;
-        const uint32_t no = tile_base + t;
-        if (!wait_warp(sm, &sm.p_ready[s], items >> s & 1)) return;
-        items ^= 1u << s;
-        if (!shared || s == 0)
-          if (!wait_warp(sm, &sm.v_full, no & 1)) return;
-        const bool first = i < 2;
-        if (first) {  // the previous segment's O of this stream has been read
-          if (!wait_warp(sm, &sm.o_free[s], (segs >> s & 1) ^ 1)) return;
-          segs ^= 1u << s;
+  for (uint32_t k = 0, issued = 0, done = 0;; ++k) {
+    const int s = k & 1;
+    if (k >= 2 && done < issued) {
+      if (v.j == v.n) {  // the next segment's values
+        if (v.n) {
+          if (elected) mbar_arrive(&sm.desc_empty[v.seg % kDescs]);
+          ++v.seg;
         }
-        tc_fence_after();
-        if (elected) {
-#pragma unroll 1
-          for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-            const uint32_t a = tmem + kColS + 128 * s + 16 * part, o = tmem + kColO + 128 * s;
-            if (first && part == 0) mma_ts<false>(o, a, vd, kIdesc);
-            else mma_ts<true>(o, a, vd, kIdesc);
-#pragma unroll
-            for (uint32_t ks = 1; ks < 8; ++ks)
-              mma_ts<true>(o, a + 32 * (ks >> 1) + 8 * (ks & 1),
-                           vd + (ks >> 2) * kPanelD + (ks & 3) * 2, kIdesc);
-          }
-          if (!shared || s == 1) mma_commit(&sm.v_empty);
-          if (i + 2 >= n_items) mma_commit(&sm.o_full[s]);
-        }
-        __syncwarp();
+        v.load(sm.desc[v.seg % kDescs]);
       }
-      if (j < n_items) {
-        const int t = shared ? j >> 1 : j;
-        const uint32_t no = tile_base + t, st = no & 1;
-        if (!shared || s == 0)
-          if (!wait_warp(sm, &sm.k_full[st], (no >> 1) & 1)) return;
-        tc_fence_after();
-        if (elected) {
-          const uint32_t d = tmem + kColS + 128 * s, k = kd + st * kTileD;
+      const uint32_t no = v.tile();
+      if (!wait_warp(sm, &sm.p_ready[s], items >> s & 1)) return;
+      items ^= 1u << s;
+      if (v.first_use())
+        if (!wait_warp(sm, &sm.v_full, no & 1)) return;
+      const bool first = v.j < 2;
+      if (first) {  // the previous segment's O of this stream has been read
+        if (!wait_warp(sm, &sm.o_free[s], (segs >> s & 1) ^ 1)) return;
+        segs ^= 1u << s;
+      }
+      tc_fence_after();
+      if (elected) {
 #pragma unroll 1
-          for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-            const uint32_t a = qd + (SPLIT ? part : q0 + (shared ? s : 0)) * kTileD;
-            if (part == 0) mma_ss<false>(d, a, k, kIdesc);
-            else mma_ss<true>(d, a, k, kIdesc);
+        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+          const uint32_t a = tmem + kColS + 128 * s + 16 * part, o = tmem + kColO + 128 * s;
+          if (first && part == 0) mma_ts<false>(o, a, vd, kIdesc);
+          else mma_ts<true>(o, a, vd, kIdesc);
 #pragma unroll
-            for (uint32_t ks = 1; ks < 8; ++ks)
-              if (ks < ksteps) {
-                const uint32_t o = (ks >> 2) * kPanelD + (ks & 3) * 2;
-                mma_ss<true>(d, a + o, k + o, kIdesc);
-              }
-          }
-          mma_commit(&sm.s_full[s]);
-          if (!shared || s == 1) mma_commit(&sm.k_empty[st]);
-          if (j == n_items - 1) {  // the segment's query rows are no longer needed
-            mma_commit(&sm.q_empty[q0]);
-            if (both) mma_commit(&sm.q_empty[q0 + 1]);
-          }
+          for (uint32_t ks = 1; ks < 8; ++ks)
+            mma_ts<true>(o, a + 32 * (ks >> 1) + 8 * (ks & 1),
+                         vd + (ks >> 2) * kPanelD + (ks & 3) * 2, kIdesc);
         }
-        __syncwarp();
+        if (v.last_use()) mma_commit(&sm.v_empty);
+        if (v.j + 2 >= v.n) mma_commit(&sm.o_full[s]);
+      }
+      __syncwarp();
+      ++v.j;
+      ++done;
+    }
+    if (more && q.j == q.n) {  // the next segment's queries
+      if (q.n) ++q.seg;
+      const uint32_t ds = q.seg % kDescs;
+      if (!wait_warp(sm, &sm.desc_full[ds], (q.seg / kDescs) & 1)) return;
+      const Desc& d = sm.desc[ds];
+      more = !d.stop;
+      if (more) {
+        q.load(d);
+        q0 = d.qslot;
+        ksteps = (min(max(d.plan.n_ranks, 1), 64) + 7) / 8;
+#pragma unroll 1
+        for (int i = q0; i < q0 + (q.shared || SPLIT ? 2 : 1); ++i) {
+          if (!wait_warp(sm, &sm.q_full[i], quse >> i & 1)) return;
+          quse ^= 1u << i;
+        }
       }
     }
-    tile_base += tiles;
-    if (elected) mbar_arrive(&sm.desc_empty[ds]);
+    if (more) {
+      const uint32_t no = q.tile(), st = no & 1;
+      if (q.first_use())
+        if (!wait_warp(sm, &sm.k_full[st], (no >> 1) & 1)) return;
+      tc_fence_after();
+      if (elected) {
+        const uint32_t d = tmem + kColS + 128 * s, kt = kd + st * kTileD;
+#pragma unroll 1
+        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+          const uint32_t a = qd + (SPLIT ? part : q0 + (q.shared ? q.j & 1 : 0)) * kTileD;
+          if (part == 0) mma_ss<false>(d, a, kt, kIdesc);
+          else mma_ss<true>(d, a, kt, kIdesc);
+#pragma unroll
+          for (uint32_t ks = 1; ks < 8; ++ks)
+            if (ks < ksteps) {
+              const uint32_t o = (ks >> 2) * kPanelD + (ks & 3) * 2;
+              mma_ss<true>(d, a + o, kt + o, kIdesc);
+            }
+        }
+        mma_commit(&sm.s_full[s]);
+        if (q.last_use()) mma_commit(&sm.k_empty[st]);
+        if (q.j + 1 == q.n) {  // the segment's query rows are no longer needed
+          mma_commit(&sm.q_empty[q0]);
+          if (q.shared || SPLIT) mma_commit(&sm.q_empty[q0 + 1]);
+        }
+      }
+      __syncwarp();
+      ++q.j;
+      ++issued;
+    } else if (done == issued) {
+      return;
+    }
   }
 }
 
@@ -1176,19 +1221,21 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
     return r;
   };
   for (uint32_t seg = 0;; ++seg) {
-    const uint32_t ds = seg & 1;
-    if (!wait_warp(sm, &sm.desc_full[ds], (seg >> 1) & 1)) return;
+    const uint32_t ds = seg % kDescs;
+    if (!wait_warp(sm, &sm.desc_full[ds], (seg / kDescs) & 1)) return;
     const Desc& d = sm.desc[ds];
     if (d.stop) return;
     const bool shared = d.shared;
-    const int tiles = d.tiles, n = shared ? tiles : (tiles - s + 1) / 2;
-    const int rows = shared ? min(128, d.rows - 128 * s) : d.rows;
+    // the segment's items alternate between the streams from stream par on: this
+    // stream has row tile f of a shared segment, else tiles f, f + 2, ...
+    const int f = s ^ d.par, tiles = d.tiles, n = shared ? tiles : (tiles - f + 1) / 2;
+    const int rows = shared ? min(128, d.rows - 128 * f) : d.rows;
     const bool active = 32 * wq < rows;  // the warp has rows
     float isc[4], m[4], l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int row = 32 * wq + g + 8 * k;  // in this stream's tile
-      const int rr = d.row0 + (shared ? 128 * s : 0) + min(row, rows - 1);
+      const int rr = d.row0 + (shared ? 128 * f : 0) + min(row, rows - 1);
       isc[k] = active ? d.isc[(d.b0 + rr / p.G) * p.a.n_q + d.h * p.G + rr % p.G] : 1.f;
       // a row past the unit's has no reference to move: its numbers go nowhere
       m[k] = row < rows ? -INFINITY : INFINITY;
@@ -1197,7 +1244,7 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
     const int len = d.len, tile0 = d.tile0;
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++items) {
-      const int t = shared ? i : 2 * i + s;
+      const int t = shared ? i : 2 * i + f;
       const uint32_t ns = (tile_base + t) % kNormSlots;
       if (!wait_warp(sm, &sm.s_full[s], items & 1)) return;
       if (active) {
@@ -1333,7 +1380,7 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
         }
         const float mr = by_row(m), lr = by_row(l);
         const int row = 32 * wq + lane;
-        const size_t at = (size_t)(s * d.sub + row);
+        const size_t at = (size_t)(f * d.sub + row);
         float* const rec_o = d.o + at * kHeadDim;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -1369,8 +1416,6 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
   grid_dep_launch();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.desc_full[i], 1);
-      mbar_init(&sm.desc_empty[i], kDescUsers);
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.k_full[i], kUnpackWarps);
@@ -1379,6 +1424,11 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
       mbar_init(&sm.p_ready[i], 4);
       mbar_init(&sm.o_full[i], 1);
       mbar_init(&sm.o_free[i], 4);
+    }
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(&sm.desc_ready[i], 1);  // the descriptor
+      mbar_init(&sm.desc_full[i], 1);   // and its plan
+      mbar_init(&sm.desc_empty[i], kDescUsers);
     }
     for (int i = 0; i < kMaxRing; ++i) {
       mbar_init(&sm.ring_full[i], 1);  // one expect_tx for the tile's records
@@ -1667,7 +1717,7 @@ cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes,
   uint8_t* const s = static_cast<uint8_t*>(ws);
   p.head = reinterpret_cast<PfxHead*>(s + w.head);
   p.cuts = reinterpret_cast<int64_t*>(s + w.cuts);
-  p.first = reinterpret_cast<PfxFirst*>(s + w.first);
+  p.first = reinterpret_cast<Unit*>(s + w.first);
   p.row = reinterpret_cast<PfxRow*>(s + w.row);
   p.unit_p = reinterpret_cast<PfxUnit*>(s + w.unit_p);
   p.unit_s = reinterpret_cast<PfxUnit*>(s + w.unit_s);
