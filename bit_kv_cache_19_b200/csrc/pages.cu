@@ -234,20 +234,27 @@ __global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(PagesParams p)
     }
     if (s_flags) atomicOr(p.status, s_flags);
   }
-  // returned pages, in sequence then row order, behind the free ones
-  for (long long i = tid; sane && i < n_ret; i += kScanThreads) {
-    int lo = 0, n = p.batch;
-    while (n > 1) {
-      const int half = n >> 1;
-      if (meta[lo + half].ret0 <= i) lo += half;
-      n -= half;
+  // returned pages, in sequence then row order, behind the free ones: a warp takes
+  // the sequences of its lanes one after the other, 32 pages at a time (a search
+  // for each page's sequence took 5 us of a 1000-request step)
+  const int lane = tid & 31;
+  for (int k = 0; k < per && sane && n_ret; ++k) {
+    const int b = b0 + k;
+    const bool mine_k = b < b1;
+    const int back = mine_k ? meta[b].ret : 0;
+    const int from = mine_k ? meta[b].held - back : 0;
+    const long long to = mine_k ? head + count + meta[b].ret0 : 0;
+    for (uint32_t any = __ballot_sync(0xffffffffu, back > 0); any; any &= any - 1) {
+      const int src = __ffs(any) - 1;
+      const int sb = __shfl_sync(0xffffffffu, b, src), n = __shfl_sync(0xffffffffu, back, src);
+      const int f = __shfl_sync(0xffffffffu, from, src);
+      const long long t0 = __shfl_sync(0xffffffffu, to, src);
+      int32_t* const row = p.table + (size_t)sb * p.max_pages + f;
+      for (int i = lane; i < n; i += 32) {
+        p.free_ids[(t0 + i) % p.n_pages] = row[i];
+        row[i] = -1;
+      }
     }
-    const PagesMeta m = meta[lo];
-    const int j = m.held - m.ret + (int)(i - m.ret0);
-    int32_t* e = p.table + (size_t)lo * p.max_pages + j;
-    const long long to = (head + count + i) % p.n_pages;
-    p.free_ids[to] = *e;
-    *e = -1;
   }
   if constexpr (SMALL) {
     __syncthreads();
