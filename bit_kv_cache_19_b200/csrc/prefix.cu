@@ -466,8 +466,11 @@ template <bool SPLIT>
 __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixParams p) {
   __shared__ PrepSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  grid_dep_launch();
+  // dependents only after the wait: a kernel that starts before this call ends
+  // (also one of another call, behind the combine) then still finds everything
+  // before this call done
   grid_dep_wait();
+  grid_dep_launch();
   if (warp == 0) {
     const bool ok = group_tables(p, sm, lane);
     if (!ok && lane == 0 && blockIdx.x == 0) atomicOr(p.a.status, KVQ_FLAG_BAD_PAGE);

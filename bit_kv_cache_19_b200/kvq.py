@@ -512,6 +512,12 @@ def _need(t, name, dtype, shape):
                                 f"{tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _ptrs(t, name, n):
+    """Refuse a pointer array (ptr_array) with fewer than n entries."""
+    if t.element_size() != 8 or t.numel() < n or not t.is_cuda:
+        raise KVQError(ERR_ARG, f"{name}: {t.numel()} device pointers for {n}")
+
+
 def make_page_state(table, held, free_ids, free_ring, page_tiles):
     """kvq_page_state over device tensors: table int32 [batch, max_pages],
     held int32 [batch], free_ids int32 [n_pages], free_ring int64 [2]."""
@@ -561,6 +567,7 @@ def paged_append_ragged(cfg, plan_ptrs, k, v, cu, slots, pool, n_pages, page_til
     _need(cu, "cu", torch.int32, (batch + 1,))
     _need(slots, "slots", torch.int64, slots.shape[:1])
     _need(lens, "lens", torch.int32, (batch,))
+    _ptrs(plan_ptrs, "plan_ptrs", batch)
     # a page holds page_tiles records of 512 (bits_k + bits_v) + 128 bytes per KV head
     if slots.shape[0] < n_rows or pool.nbytes < \
             n_pages * page_tiles * cfg.n_kv_heads * (512 * (cfg.bits_k + cfg.bits_v) + 128):
@@ -581,7 +588,7 @@ def prefix_decode_workspace_bytes(cfg, batch, n_q_heads, n_prefixes) -> int:
                                                    n_prefixes)
 
 
-def _prefix_args(prefix_lens, group_start, lens, q, out):
+def _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out):
     import torch
     batch, n_prefixes = lens.shape[0], prefix_lens.shape[0]
     rows = (batch, q.shape[1], 128)
@@ -590,6 +597,7 @@ def _prefix_args(prefix_lens, group_start, lens, q, out):
     _need(lens, "lens", torch.int32, (batch,))
     _need(q, "q", q.dtype, rows)
     _need(out, "out", out.dtype, rows)
+    _ptrs(plan_ptrs, "plan_ptrs", batch)
     return batch, n_prefixes
 
 
@@ -598,7 +606,9 @@ def prefix_decode_attn(cfg, plan_ptrs, prefix_ptrs, prefix_lens, group_start, ma
     """Decode q [batch, n_q, 128] into out (bf16, fp16 or fp32) over each
     group's shared prefix cache (sequences group_start[g] .. group_start[g + 1]
     - 1 share prefix g) and each sequence's own cache."""
-    batch, n_prefixes = _prefix_args(prefix_lens, group_start, lens, q, out)
+    batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out)
+    _ptrs(prefix_ptrs, "prefix_ptrs", n_prefixes)
+    _ptrs(cache_ptrs, "cache_ptrs", batch)
     rc = lib().kvq_prefix_decode_attn(
         cfg, plan_ptrs.data_ptr(), prefix_ptrs.data_ptr(), prefix_lens.data_ptr(),
         group_start.data_ptr(), n_prefixes, max_prefix_len, cache_ptrs.data_ptr(),
@@ -613,7 +623,7 @@ def paged_prefix_decode_attn(cfg, plan_ptrs, prefix_pages, prefix_lens, group_st
                              max_prefix_len, pages, lens, max_len, q, out, ws, status):
     """prefix_decode_attn over paged caches (the prefixes' block-table rows in
     prefix_pages, the sequences' in pages)."""
-    batch, n_prefixes = _prefix_args(prefix_lens, group_start, lens, q, out)
+    batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out)
     rc = lib().kvq_paged_prefix_decode_attn(
         cfg, plan_ptrs.data_ptr(), prefix_pages, prefix_lens.data_ptr(), group_start.data_ptr(),
         n_prefixes, max_prefix_len, pages, lens.data_ptr(), batch, max_len, q.data_ptr(),
