@@ -1200,6 +1200,11 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
   }
 }
 
+template <int N>
+struct IntC {
+  __device__ constexpr operator int() const { return N; }
+};
+
 // Softmax of stream s (one warpgroup, 32 rows per warp). A chunk of 32 columns
 // (one record) is held like a matrix fragment: lane (g, q) = (lane / 4, lane mod
 // 4) has rows g + 8 k (k < 4) and columns 8 j + 2 q + (0, 1) (j < 4), so that a
@@ -1257,22 +1262,24 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
         // code of the roles outgrew the instruction cache. P = 2^(s - m) times the
         // value norm goes in place of the logits: the pairs of columns 32 c .. to
         // columns 32 c .. + 15 (low parts + 16 ..)
+        auto chunks = [&](auto groups) {
+          constexpr int K = groups;  // groups of 8 rows that hold any (1, or up to 4)
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[2][16];
           tmem_ld_frag(ts + 32 * c, v[0]);
-          tmem_ld_frag(ts + (16u << 16) + 32 * c, v[1]);
+          if constexpr (K > 2) tmem_ld_frag(ts + (16u << 16) + 32 * c, v[1]);
           const float2* nk2 = reinterpret_cast<const float2*>(&sm.nk[ns][32 * c + 2 * q]);
           const float2* nv2 = reinterpret_cast<const float2*>(&sm.nv[ns][32 * c + 2 * q]);
           const float lg = (float)sm.lg[ns][c];
           const float2 nk[4] = {nk2[0], nk2[4], nk2[8], nk2[12]};
           tmem_wait_ld16(v[0]);
-          tmem_wait_ld16(v[1]);
+          if constexpr (K > 2) tmem_wait_ld16(v[1]);
           float2 u[4][4];  // [row k][column group j]: logits times key norms
           float top[4];
           bool move = false;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < K; ++k) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int e = 4 * j + 2 * (k & 1);
@@ -1282,7 +1289,7 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
           }
           if (nvalid < 32 * c + 32) {  // the last tile: positions past the end
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < K; ++k)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 if (32 * c + 8 * j + 2 * q >= nvalid) u[k][j].x = -INFINITY;
@@ -1290,7 +1297,7 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
               }
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < K; ++k) {
             const float a = fmaxf(fmaxf(u[k][0].x, u[k][0].y), u[k][1].x);
             const float b = fmaxf(fmaxf(u[k][1].y, u[k][2].x), u[k][2].y);
             top[k] = fmaxf(fmaxf(a, b), fmaxf(u[k][3].x, u[k][3].y)) * isc[k] + lg;
@@ -1300,9 +1307,9 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
           // 2^kPTop (or on NaN): O, l and this tile's earlier P are scaled by a
           // power of two
           if (nvalid > 32 * c && __any_sync(0xffffffffu, move)) {
-            float alpha[4];
+            float alpha[4] = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < K; ++k) {
               top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
               top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
               const bool mv = !(top[k] - m[k] <= kPTop);
@@ -1337,9 +1344,9 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
               tmem_st8(ts + 8 * k, o);
             }
           }
-          uint32_t hi[2][8], lo[2][SPLIT ? 8 : 1];
+          uint32_t hi[2][8] = {}, lo[2][SPLIT ? 8 : 1] = {};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < K; ++k) {
             const float2 is = make_float2(isc[k], isc[k]), nm = make_float2(-m[k], -m[k]);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -1359,12 +1366,15 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
             l[k] += sum.x + sum.y;
           }
           tmem_st_frag(ts + 32 * c, hi[0]);
-          tmem_st_frag(ts + (16u << 16) + 32 * c, hi[1]);
+          if constexpr (K > 2) tmem_st_frag(ts + (16u << 16) + 32 * c, hi[1]);
           if constexpr (SPLIT) {
             tmem_st_frag(ts + 32 * c + 16, lo[0]);
-            tmem_st_frag(ts + (16u << 16) + 32 * c + 16, lo[1]);
+            if constexpr (K > 2) tmem_st_frag(ts + (16u << 16) + 32 * c + 16, lo[1]);
           }
         }
+        };
+        if (rows - 32 * wq <= 8) chunks(IntC<1>{});
+        else chunks(IntC<4>{});
         tmem_wait_st();
         tc_fence_before();
       }
