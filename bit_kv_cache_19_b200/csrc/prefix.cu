@@ -1344,7 +1344,8 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
               tmem_st8(ts + 8 * k, o);
             }
           }
-          uint32_t hi[2][8] = {}, lo[2][SPLIT ? 8 : 1] = {};
+          uint32_t hi[2][8] = {};
+          [[maybe_unused]] uint32_t lo[2][SPLIT ? 8 : 1] = {};
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             const float2 is = make_float2(isc[k], isc[k]), nm = make_float2(-m[k], -m[k]);
