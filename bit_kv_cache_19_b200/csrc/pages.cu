@@ -16,7 +16,9 @@
 // prefill chunk the store rate. Split: one CTA makes the three prefix sums (they
 // are serial over the batch); a small step is finished by that CTA (one launch),
 // a larger one by a grid over tokens and pages that resolves new pages from the
-// ring itself, so that it waits for nothing but the sums.
+// ring itself, so that it waits for nothing but the sums. Measured: 5.2 us for 256
+// one-token requests; 18 us, with a copy that resets the state, for 482499 tokens
+// of 1000 requests.
 #include <algorithm>
 
 #include "pages.cuh"
@@ -277,7 +279,9 @@ __global__ void __launch_bounds__(256) pages_map_kernel(PagesParams p) {
 size_t pages_workspace_bytes(int batch) { return 256 + (size_t)batch * sizeof(PagesMeta); }
 
 // One launch while the scan's CTA can also write the slots in about the time a
-// second launch takes to start.
+// second launch takes to start. One launch / two, us on the GPU: 256 requests of a
+// token 5.2 / 7.8; 2160 slots of 9 requests 5.9 / 6.8; 4096 of 64 8.8 / 9.3; 6300 of 9
+// 8.0 / 6.4; 16384 of 64 17.5 / 9.9.
 constexpr int64_t kOneLaunchSlots = 4096;
 
 cudaError_t launch_pages_assign(PagesParams p, void* ws, cudaStream_t st) {

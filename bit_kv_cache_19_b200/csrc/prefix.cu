@@ -17,7 +17,7 @@
 // multiplies the fp32 logit. V = the centroids of the rotated values, P =
 // 2^(s - m) times the value norm, in fp16. The inverse rotation comes after
 // the merge. Rounding: for bf16 outputs Q and P are rounded to fp16 once (2^-11
-// relative at most each, well under the output's 2^-9); for fp16 and fp32
+// relative at most each, an eighth of the output's own 2^-8); for fp16 and fp32
 // outputs both are split into two fp16 terms (hi + lo), two products each.
 //
 // Three launches (programmatic dependent launch between them):
@@ -33,9 +33,14 @@
 //     one gives the streams alternate tiles. TMEM: S of both streams (P
 //     overwrites it) and O of both, 512 columns.
 //  3. combine: merges each row's records, undoes the value rotation.
-// What bounds it: shared-memory bandwidth of unpacking (codebook lookups, tile
-// stores, operand reads) at few rows; the exponentials and the tensor cores at
-// 256 rows.
+// What bounds it: no unit is near its peak. Tensor memory is full, so a stream's
+// P overwrites its S and its products and softmax take turns; that chain takes
+// about 4000 cycles per 128-token tile at few rows and 6500 to 7000 at 256 rows
+// (exponentials and tensor cores: 2048 each at their peak rates). Measured: 64
+// sequences behind one prefix of 131072 tokens, 16 query heads on 2 KV heads, K3V3:
+// 153 us, 455 TFLOP/s of useful products; 48 sequences over three prefixes (32 on 8
+// heads, K2V2, 14.4 MB): 57 us, of which main 45, prep and combine 7 each. There 37 %
+// of issue slots and 16 % of the tensor pipe's cycles are used.
 #include <algorithm>
 #include <cstddef>
 
@@ -66,7 +71,9 @@ constexpr uint32_t kColS = 0, kColO = 256;
 // P is kept below 2^kPTop; a softmax reference moves when a tile would pass it,
 // to leave the tile's largest P at 2^kPSet
 constexpr float kPTop = 15.f, kPSet = 7.f;
-// cost of a segment's start and of one tile (shared: 256 rows; else <= 128)
+// cost of a segment's start and of one tile (shared: 256 rows; else <= 128), near
+// the measured 4.6k to 5.3k, 6.5k to 7k and 4k cycles; 4 : 6 for the tiles and 5 for
+// the start took 153 us instead of 150 for a 131072-token prefix
 constexpr int kCostSeg = 3, kCostShared = 5, kCostAlt = 3;
 constexpr int kDescs = 4;  // segments in flight
 

@@ -9,6 +9,12 @@
 // touches at most n / 32 + 2 tiles, so item numbers start at cu[b] / 32 + 2 b for
 // sequence b, a bound that follows from cu alone: a CTA finds its sequence by
 // bisection, without a prefix sum over lengths.
+//
+// What bounds it: instruction issue (69 % of slots; 17400 warp instructions per
+// tile and KV head: norms, divisions and roots per token, shared atomics to pack),
+// like the bulk quantizer. Measured: 52892 tokens of 24 sequences, 8 KV heads, K2V2,
+// bf16: 300 us for 246 MB, 820 GB/s; one token for each of 16 sequences 10 us (the
+// latency of one tile, with a copy that resets the lengths).
 #include <algorithm>
 
 #include "bulk_dev.cuh"
