@@ -518,6 +518,13 @@ def _ptrs(t, name, n):
         raise KVQError(ERR_ARG, f"{name}: {t.numel()} device pointers for {n}")
 
 
+def _on_device(**tensors):
+    """Refuse memory that the GPU cannot address: the library only sees addresses."""
+    for name, t in tensors.items():
+        if not t.is_cuda:
+            raise KVQError(ERR_ARG, f"{name}: on {t.device}, not on a GPU")
+
+
 def make_page_state(table, held, free_ids, free_ring, page_tiles):
     """kvq_page_state over device tensors: table int32 [batch, max_pages],
     held int32 [batch], free_ids int32 [n_pages], free_ring int64 [2]."""
@@ -526,8 +533,10 @@ def make_page_state(table, held, free_ids, free_ring, page_tiles):
     _need(held, "held", torch.int32, table.shape[:1])
     _need(free_ids, "free_ids", torch.int32, free_ids.shape[:1])
     _need(free_ring, "free_ring", torch.int64, (2,))
-    return PageState(table.data_ptr(), held.data_ptr(), free_ids.data_ptr(), free_ring.data_ptr(),
-                     free_ids.shape[0], page_tiles, table.shape[1])
+    state = PageState(table.data_ptr(), held.data_ptr(), free_ids.data_ptr(),
+                      free_ring.data_ptr(), free_ids.shape[0], page_tiles, table.shape[1])
+    state.rows = table.shape[0]  # for the checks of pages_assign
+    return state
 
 
 def pages_assign_workspace_bytes(batch) -> int:
@@ -548,6 +557,9 @@ def pages_assign(state, lens, n_new, cu, slots, pos, ws, status):
     if pos is not None:
         _need(pos, "pos", i32, (n_slots,))
         pos = pos.data_ptr()
+    _on_device(ws=ws, status=status)
+    if batch != getattr(state, "rows", batch):
+        raise KVQError(ERR_ARG, f"{batch} sequences, block table of {state.rows} rows")
     rc = lib().kvq_pages_assign(state, lens.data_ptr(), n_new.data_ptr(), batch, n_slots,
                                 cu.data_ptr(), slots.data_ptr(), pos, ws.data_ptr(), ws.nbytes,
                                 status.data_ptr(), _stream_of(lens))
@@ -567,6 +579,7 @@ def paged_append_ragged(cfg, plan_ptrs, k, v, cu, slots, pool, n_pages, page_til
     _need(cu, "cu", torch.int32, (batch + 1,))
     _need(slots, "slots", torch.int64, slots.shape[:1])
     _need(lens, "lens", torch.int32, (batch,))
+    _on_device(pool=pool, status=status)
     _ptrs(plan_ptrs, "plan_ptrs", batch)
     # a page holds page_tiles records of 512 (bits_k + bits_v) + 128 bytes per KV head
     if slots.shape[0] < n_rows or pool.nbytes < \
@@ -588,7 +601,7 @@ def prefix_decode_workspace_bytes(cfg, batch, n_q_heads, n_prefixes) -> int:
                                                    n_prefixes)
 
 
-def _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out):
+def _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws, status):
     import torch
     batch, n_prefixes = lens.shape[0], prefix_lens.shape[0]
     rows = (batch, q.shape[1], 128)
@@ -598,6 +611,7 @@ def _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out):
     _need(q, "q", q.dtype, rows)
     _need(out, "out", out.dtype, rows)
     _ptrs(plan_ptrs, "plan_ptrs", batch)
+    _on_device(ws=ws, status=status)
     return batch, n_prefixes
 
 
@@ -606,7 +620,8 @@ def prefix_decode_attn(cfg, plan_ptrs, prefix_ptrs, prefix_lens, group_start, ma
     """Decode q [batch, n_q, 128] into out (bf16, fp16 or fp32) over each
     group's shared prefix cache (sequences group_start[g] .. group_start[g + 1]
     - 1 share prefix g) and each sequence's own cache."""
-    batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out)
+    batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws,
+                                      status)
     _ptrs(prefix_ptrs, "prefix_ptrs", n_prefixes)
     _ptrs(cache_ptrs, "cache_ptrs", batch)
     rc = lib().kvq_prefix_decode_attn(
@@ -623,7 +638,8 @@ def paged_prefix_decode_attn(cfg, plan_ptrs, prefix_pages, prefix_lens, group_st
                              max_prefix_len, pages, lens, max_len, q, out, ws, status):
     """prefix_decode_attn over paged caches (the prefixes' block-table rows in
     prefix_pages, the sequences' in pages)."""
-    batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out)
+    batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws,
+                                      status)
     rc = lib().kvq_paged_prefix_decode_attn(
         cfg, plan_ptrs.data_ptr(), prefix_pages, prefix_lens.data_ptr(), group_start.data_ptr(),
         n_prefixes, max_prefix_len, pages, lens.data_ptr(), batch, max_len, q.data_ptr(),

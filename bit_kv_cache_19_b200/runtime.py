@@ -179,6 +179,7 @@ class PackedLayer:
         tokens: sequences group_start[g] .. group_start[g + 1] - 1 (int32, device)
         share sequence g of ``prefix``, another PackedLayer with the same plans.
         out: q's type unless given (bf16, fp16 or fp32)."""
+        _same_format(self, prefix)
         if out is None:
             out = torch.empty_like(q)
         if ws is None:
@@ -209,6 +210,13 @@ class PackedLayer:
 
     def flags(self) -> int:
         return int(self.status.item()) & 0xFFFFFFFF
+
+
+def _same_format(layer, prefix) -> None:
+    """A prefix is read with its layer's record size and head count."""
+    a, b = layer.cfg, prefix.cfg
+    if (a.n_kv_heads, a.bits_k, a.bits_v) != (b.n_kv_heads, b.bits_k, b.bits_v):
+        raise ValueError("the prefix's KV heads or bits are not the layer's")
 
 
 def prefix_workspace(cfg, batch: int, n_q: int, n_prefixes: int, device="cuda"):
@@ -408,6 +416,7 @@ class PagedLayer:
         tokens: sequences group_start[g] .. group_start[g + 1] - 1 (int32, device)
         share row g of ``prefix``, another PagedLayer with the same plans. out:
         q's type unless given (bf16, fp16 or fp32)."""
+        _same_format(self, prefix)
         if out is None:
             out = torch.empty_like(q)
         if ws is None:

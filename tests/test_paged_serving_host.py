@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from bit_kv_cache_19_b200 import kvq
-from bit_kv_cache_19_b200.runtime import PagedLayer
+from bit_kv_cache_19_b200.runtime import PackedLayer, PagedLayer
 
 A = ctypes.create_string_buffer(1 << 12)
 BASE = (ctypes.addressof(A) + 511) & ~511  # a non-null, aligned address; never read
@@ -123,3 +123,36 @@ def test_layer_on_host_pages_refuses_device_assignment():
         L.reserve(0, 5)
     with pytest.raises(RuntimeError):
         L.release(0)
+
+
+def test_host_memory_is_not_passed_to_the_gpu(monkeypatch):
+    """Workspaces, status words and pools on the host, and lengths of another
+    batch than the block table's, raise before the library is called."""
+    def no_call():
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(kvq, "_need", lambda *a: None)
+    monkeypatch.setattr(kvq, "_ptrs", lambda *a: None)
+    monkeypatch.setattr(kvq, "lib", no_call)
+    i, x, cfg = torch.zeros(3, dtype=torch.int32), torch.zeros(3, 2, 128), kvq.make_cfg(2, 3, 3)
+    page = torch.zeros(1 << 14, dtype=torch.uint8)
+    calls = [lambda: kvq.pages_assign(_state(), i, i, i, i, None, i, i),
+             lambda: kvq.paged_append_ragged(cfg, i, x, x, i, i, page, 1, 1, i, i),
+             lambda: kvq.prefix_decode_attn(cfg, i, i, i, i, 4, i, i, 4, x, x, x, i),
+             lambda: kvq.paged_prefix_decode_attn(cfg, i, None, i, i, 4, None, i, 4, x, x, x, i)]
+    for call in calls:
+        with pytest.raises(kvq.KVQError, match="not on a GPU"):
+            call()
+    monkeypatch.setattr(kvq, "_on_device", lambda **k: None)
+    state = kvq.make_page_state(torch.zeros(4, 2, dtype=torch.int32), i, i, i, 1)
+    with pytest.raises(kvq.KVQError, match="block table of 4 rows"):
+        kvq.pages_assign(state, i, i, i, i, None, i, i)
+
+
+@pytest.mark.parametrize("kind", [PackedLayer, PagedLayer])
+@pytest.mark.parametrize("other", [(1, 3, 3), (2, 2, 3), (2, 3, 2)])
+def test_prefix_of_another_format(kind, other):
+    L, P = kind.__new__(kind), kind.__new__(kind)
+    L.cfg, P.cfg = kvq.make_cfg(2, 3, 3), kvq.make_cfg(*other)
+    with pytest.raises(ValueError, match="heads or bits"):
+        L.decode_prefix(None, P, None)
