@@ -243,3 +243,22 @@ def test_serving_loop_in_a_graph():
         assert (C.lens - pre).tolist() == P.lens.tolist()
         first = False
     assert P.flags() == 0 and P.dev_pages.flags() == 0 and C.flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_rows_at_an_odd_address(dtype):
+    rng, cfg, E, plans = setup(31, 2, 3, 2)
+    n_new = [33, 0, 7]
+    got = []
+    for off in (0, 1):
+        P = layer(cfg, plans, 3, 1, 4)
+        if not off:
+            k, v = rows(rng, 40, 2, E, dtype)
+        else:
+            k, v = (torch.cat([x.new_zeros(1), x.flatten()])[1:].view(x.shape) for x in (k, v))
+            assert k.data_ptr() % 16 != 0 and v.data_ptr() % 16 != 0
+        cu, slots, _ = P.assign(torch.tensor(n_new, **I32), 40)
+        P.append_ragged(k, v, cu, slots)
+        assert P.flags() == 0
+        got.append(P.pool.clone())
+    assert torch.equal(got[0], got[1])

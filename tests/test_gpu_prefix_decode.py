@@ -395,3 +395,37 @@ def test_pages_past_four_gigabytes():
         L.append_ragged(k, v, cu, slots)
         far.append(L)
     assert torch.equal(far[1].decode_prefix(q, far[0], gs), want) and far[1].flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_query_at_an_odd_address_and_output_in_its_place(dtype):
+    S = Setup(23, 2, 3, 3)
+    pre, own = [200], [40, 0, 131]
+    P, Q = contiguous(S, pre, [S.tokens(200)]), contiguous(S, own, [S.tokens(n) for n in own])
+    gs = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    q = torch.from_numpy(S.rng.standard_normal((3, 8, 128))).to(dtype).to(DEV)
+    want = Q.decode_prefix(q, P, gs)
+    odd = torch.empty(q.numel() + 1, dtype=dtype, device=DEV)[1:].view(q.shape)
+    odd.copy_(q)
+    assert odd.data_ptr() % 16 != 0
+    assert torch.equal(Q.decode_prefix(odd, P, gs, out=torch.empty_like(q)), want)
+    with pytest.raises(kvq.KVQError):  # outputs are stored 16 bytes at a time
+        Q.decode_prefix(q, P, gs, out=odd)
+    for _ in range(5):
+        x = q.clone()
+        assert torch.equal(Q.decode_prefix(x, P, gs, out=x), want)
+    assert Q.flags() == 0
+
+
+def test_short_pointer_arrays_are_refused():
+    S = Setup(29, 1, 2, 2)
+    P, Q = contiguous(S, [40], [S.tokens(40)]), contiguous(S, [5, 6], [S.tokens(5), S.tokens(6)])
+    gs = torch.tensor([0, 2], dtype=torch.int32, device=DEV)
+    q = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device=DEV)
+    ws = prefix_workspace(S.cfg, 2, 4, 1)
+    for plans, pre, own in ((Q.plan_ptrs[:1], P.cache_ptrs, Q.cache_ptrs),
+                            (Q.plan_ptrs, P.cache_ptrs[:0], Q.cache_ptrs),
+                            (Q.plan_ptrs, P.cache_ptrs, Q.cache_ptrs[:1])):
+        with pytest.raises(kvq.KVQError):
+            kvq.prefix_decode_attn(S.cfg, plans, pre, P.lens, gs, P.cap, own, Q.lens, Q.cap, q,
+                                   torch.empty_like(q), ws, Q.status)
