@@ -1314,6 +1314,10 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
           // 2^kPTop (or on NaN): O, l and this tile's earlier P are scaled by a
           // power of two
           if (nvalid > 32 * c && __any_sync(0xffffffffu, move)) {
+            // what is read back below may have been stored by this tile's earlier
+            // chunks (their P, and O and P of an earlier move): stores are
+            // asynchronous, and only this wait orders a later load behind them
+            tmem_wait_st();
             float alpha[4] = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
             for (int k = 0; k < K; ++k) {
