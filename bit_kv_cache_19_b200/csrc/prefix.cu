@@ -641,6 +641,13 @@ __device__ __forceinline__ KeyStep key_step(const Plan& pl, int hs, int lane) {
   return k;
 }
 
+// Least e with norm < 2^e (a stored norm: fp16, >= 0). 0 counts as 2^-64: such a
+// token adds nothing to O, so that any reference suits it as long as its weight,
+// below 2^(kPTop + 64), and the sum of 2^31 of them stay finite.
+__device__ __forceinline__ int norm_exp(float norm) {
+  return max((int)(__float_as_uint(norm) >> 23) - 126, -64);
+}
+
 // One half step of the four records whose key words are at w, into the K tile
 // at dst (32 rows each). The records are independent lookup chains, which hides their latency; a tile's missing
 // records repeat earlier ones (their positions are masked in the softmax).
@@ -1045,7 +1052,7 @@ __device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm,
           sm.nk[ns][32 * me + lane] = kn;
           sm.nv[ns][32 * me + lane] = vn;
           const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(vn));
-          if (lane == 0) sm.lg[ns][me] = max((int)(mx >> 23) - 126, -24);
+          if (lane == 0) sm.lg[ns][me] = norm_exp(__uint_as_float(mx));
         }
         fence_proxy_async();
         __syncwarp();
@@ -1283,7 +1290,6 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
           tmem_wait_ld16(v[0]);
           if constexpr (K > 2) tmem_wait_ld16(v[1]);
           float2 u[4][4];  // [row k][column group j]: logits times key norms
-          float top[4];
           bool move = false;
 #pragma unroll
           for (int k = 0; k < K; ++k) {
@@ -1307,52 +1313,69 @@ __device__ __forceinline__ void softmax_role(const PrefixParams& p, MainSmem& sm
           for (int k = 0; k < K; ++k) {
             const float a = fmaxf(fmaxf(u[k][0].x, u[k][0].y), u[k][1].x);
             const float b = fmaxf(fmaxf(u[k][1].y, u[k][2].x), u[k][2].y);
-            top[k] = fmaxf(fmaxf(a, b), fmaxf(u[k][3].x, u[k][3].y)) * isc[k] + lg;
-            move |= 32 * wq + g + 8 * k < rows && !(top[k] - m[k] <= kPTop);
+            const float top = fmaxf(fmaxf(a, b), fmaxf(u[k][3].x, u[k][3].y)) * isc[k] + lg;
+            move |= 32 * wq + g + 8 * k < rows && !(top - m[k] <= kPTop);
           }
           // the reference, a whole number, moves only when a product would pass
-          // 2^kPTop (or on NaN): O, l and this tile's earlier P are scaled by a
-          // power of two
+          // 2^kPTop (or on NaN), to leave the largest product so far between
+          // 2^(kPSet - 2) and 2^kPTop: O, l and this tile's earlier P are scaled by a
+          // power of two. The bound above takes the chunk's largest value norm; what
+          // decides is each token's own, or the reference would follow a heavy token
+          // of small norm and leave the others' products below fp16's normal range
           if (nvalid > 32 * c && __any_sync(0xffffffffu, move)) {
-            // what is read back below may have been stored by this tile's earlier
-            // chunks (their P, and O and P of an earlier move): stores are
-            // asynchronous, and only this wait orders a later load behind them
-            tmem_wait_st();
             float alpha[4] = {1.f, 1.f, 1.f, 1.f};
+            bool moved = false;
+            float2 e[4];  // the value norms are below 2^e
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              e[j] = make_float2((float)norm_exp(nv2[4 * j].x), (float)norm_exp(nv2[4 * j].y));
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-              top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
-              top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
-              const bool mv = !(top[k] - m[k] <= kPTop);
-              const float m_new = mv ? ceilf(top[k]) - kPSet : m[k];
-              alpha[k] = mv ? ex2(m[k] - m_new) : 1.f;  // 0 from -inf
-              l[k] *= alpha[k];
-              m[k] = m_new;
+              float t = fmaxf(fmaf(u[k][0].x, isc[k], e[0].x), fmaf(u[k][0].y, isc[k], e[0].y));
+#pragma unroll
+              for (int j = 1; j < 4; ++j)
+                t = fmaxf(t, fmaxf(fmaf(u[k][j].x, isc[k], e[j].x),
+                                   fmaf(u[k][j].y, isc[k], e[j].y)));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+              if (!(t - m[k] <= kPTop)) {
+                const float m_new = ceilf(t) - kPSet;
+                alpha[k] = ex2(m[k] - m_new);  // 0 from -inf
+                l[k] *= alpha[k];
+                m[k] = m_new;
+                moved = true;
+              }
             }
-            const float ar = by_row(alpha);
-            if (i > 0) {  // O holds this segment's earlier tiles
+            if (__any_sync(0xffffffffu, moved)) {
+              // what is read back below may have been stored by this tile's earlier
+              // chunks (their P, and O and P of an earlier move): stores are
+              // asynchronous, and only this wait orders a later load behind them
+              tmem_wait_st();
+              const float ar = by_row(alpha);
+              if (i > 0) {  // O holds this segment's earlier tiles
 #pragma unroll 1
-              for (int k = 0; k < 16; ++k) {
+                for (int k = 0; k < 16; ++k) {
+                  uint32_t o[8];
+                  tmem_ld8(to + 8 * k, o);
+                  tmem_wait_ld8(o);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ar);
+                  tmem_st8(to + 8 * k, o);
+                }
+              }
+              const __half2 ah = __float2half2_rn(ar);
+#pragma unroll 1
+              for (int k = 0; k < 4 * c; ++k) {  // columns 0 .. 31 of each earlier record
                 uint32_t o[8];
-                tmem_ld8(to + 8 * k, o);
+                tmem_ld8(ts + 8 * k, o);
                 tmem_wait_ld8(o);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ar);
-                tmem_st8(to + 8 * k, o);
+                for (int e = 0; e < 8; ++e) {
+                  const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), ah);
+                  o[e] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+                tmem_st8(ts + 8 * k, o);
               }
-            }
-            const __half2 ah = __float2half2_rn(ar);
-#pragma unroll 1
-            for (int k = 0; k < 4 * c; ++k) {  // columns 0 .. 31 of each earlier record
-              uint32_t o[8];
-              tmem_ld8(ts + 8 * k, o);
-              tmem_wait_ld8(o);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), ah);
-                o[e] = *reinterpret_cast<const uint32_t*>(&x);
-              }
-              tmem_st8(ts + 8 * k, o);
             }
           }
           uint32_t hi[2][8] = {};
