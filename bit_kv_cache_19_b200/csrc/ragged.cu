@@ -88,9 +88,11 @@ __device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& p, int64_t
   const int64_t slot = p.slots[it.row];
   if (slot == -1) return it;
   const int64_t page = slot >> p.span_shift;
-  const int in_page = (int)(slot & (p.span - 1));
-  if (slot < 0 || page >= p.n_pages || (in_page & (kTile - 1)) != it.p_lo ||
-      p.slots[it.row + it.n - 1] != slot + it.n - 1) {
+  const int in_page = (int)(slot & (p.span - 1)), lane = threadIdx.x & 31;
+  // every warp looks at all of the tile's slots, a lane at one
+  const bool run =
+      __all_sync(0xffffffffu, lane >= it.n || p.slots[it.row + lane] == slot + lane);
+  if (slot < 0 || page >= p.n_pages || (in_page & (kTile - 1)) != it.p_lo || !run) {
     it.flags = KVQ_FLAG_BAD_PAGE;
     return it;
   }
