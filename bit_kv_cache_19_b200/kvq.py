@@ -345,13 +345,30 @@ def page_bytes(cfg, page_tiles) -> int:
 def make_pages(pool, block_table, n_pages, page_tiles):
     """kvq_pages over a device pool (n_pages pages of page_bytes) and a device
     block table int32 [batch, max_pages]."""
-    return Pages(pool.data_ptr(), block_table.data_ptr(), n_pages, page_tiles,
-                 block_table.shape[1])
+    import torch
+    _need(block_table, "block_table", torch.int32, (block_table.shape[0], block_table.shape[-1]))
+    pages = Pages(pool.data_ptr(), block_table.data_ptr(), n_pages, page_tiles,
+                  block_table.shape[1])
+    # for the checks of the calls that follow the table: its rows, and the bytes
+    # that the pool has for a tile's records of all KV heads
+    pages.rows, pages.tile_room = block_table.shape[0], pool.nbytes // max(n_pages * page_tiles, 1)
+    return pages
+
+
+def _pages(cfg, pages, name, rows):
+    """Refuse a block table of fewer rows than the call's sequences, or a pool
+    shorter than its pages (make_pages; a bare Pages says neither)."""
+    if getattr(pages, "rows", rows) < rows:
+        raise KVQError(ERR_ARG, f"{name}: block table of {pages.rows} rows for {rows}")
+    need = cfg.n_kv_heads * (512 * (cfg.bits_k + cfg.bits_v) + 128)
+    if getattr(pages, "tile_room", need) < need:
+        raise KVQError(ERR_ARG, f"{name}: pool of {pages.tile_room} bytes a tile for {need}")
 
 
 def paged_quantize_append(cfg, plan_ptrs, k, v, pages, lens, status, rope_base=0.0):
     """kvq_quantize_append into paged caches (rope_base > 1: pre-RoPE keys)."""
     batch, n_new = k.shape[0], k.shape[1]
+    _pages(cfg, pages, "pages", batch)
     _check(lib().kvq_paged_quantize_append(ctypes.byref(cfg), _ptr(plan_ptrs), _ptr(k), _ptr(v),
                                            _dtype_code(k), batch, n_new, ctypes.byref(pages),
                                            _ptr(lens), float(rope_base), _ptr(status),
@@ -361,6 +378,7 @@ def paged_quantize_append(cfg, plan_ptrs, k, v, pages, lens, status, rope_base=0
 def paged_decode_attn(cfg, plan_ptrs, pages, lens, max_len, q, out, ws, status):
     """kvq_decode_attn over paged caches."""
     batch, n_q = q.shape[0], q.shape[1]
+    _pages(cfg, pages, "pages", batch)
     _check(lib().kvq_paged_decode_attn(ctypes.byref(cfg), _ptr(plan_ptrs), ctypes.byref(pages),
                                        _ptr(lens), batch, max_len, _ptr(q), _dtype_code(q), n_q,
                                        _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
@@ -370,6 +388,7 @@ def paged_decode_attn(cfg, plan_ptrs, pages, lens, max_len, q, out, ws, status):
 def paged_decode_attn_partial(cfg, plan_ptrs, pages, lens, max_len, q, rec, ws, status):
     """kvq_decode_attn_partial over paged caches: records fp32 [batch, n_q, 132]."""
     batch, n_q = q.shape[0], q.shape[1]
+    _pages(cfg, pages, "pages", batch)
     _check(lib().kvq_paged_decode_attn_partial(ctypes.byref(cfg), _ptr(plan_ptrs),
                                                ctypes.byref(pages), _ptr(lens), batch, max_len,
                                                _ptr(q), _dtype_code(q), n_q, _ptr(rec), _ptr(ws),
@@ -382,6 +401,7 @@ def paged_append_decode(cfg, plan_ptrs, k, v, pages, lens, max_len, q, out, ws, 
     """kvq_append_decode over paged caches."""
     batch, n_q = q.shape[0], q.shape[1]
     n_new = 0 if k is None else k.shape[1]
+    _pages(cfg, pages, "pages", batch)
     _check(lib().kvq_paged_append_decode(ctypes.byref(cfg), _ptr(plan_ptrs), _ptr(k), _ptr(v),
                                          _dtype_code(k) if k is not None else BF16, n_new,
                                          ctypes.byref(pages), _ptr(lens), batch, max_len,
@@ -640,6 +660,8 @@ def paged_prefix_decode_attn(cfg, plan_ptrs, prefix_pages, prefix_lens, group_st
     prefix_pages, the sequences' in pages)."""
     batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws,
                                       status)
+    _pages(cfg, prefix_pages, "prefix_pages", n_prefixes)
+    _pages(cfg, pages, "pages", batch)
     rc = lib().kvq_paged_prefix_decode_attn(
         cfg, plan_ptrs.data_ptr(), prefix_pages, prefix_lens.data_ptr(), group_start.data_ptr(),
         n_prefixes, max_prefix_len, pages, lens.data_ptr(), batch, max_len, q.data_ptr(),

@@ -1,0 +1,86 @@
+"""The Python binding's checks of what the library cannot see behind an address: block
+tables and pools that are too short. On the CPU: the library is never called."""
+import pytest
+import torch
+
+from bit_kv_cache_19_b200 import kvq
+
+CFG = kvq.make_cfg(2, 3, 2)
+PAGE = 4 * 2 * (512 * 5 + 128)  # four tiles of two KV heads
+
+
+class OnGpu:
+    """A CPU tensor that says it is on a GPU; only its address is taken."""
+
+    def __init__(self, tensor, device=0):
+        self.tensor, self.where = tensor, device
+        self.is_cuda, self.device = True, f"cuda:{device}"
+
+    def get_device(self):
+        return self.where
+
+    def __getattr__(self, name):
+        return getattr(self.tensor, name)
+
+
+@pytest.fixture
+def no_call(monkeypatch):
+    def called():
+        raise AssertionError("the library was called")
+    monkeypatch.setattr(kvq, "lib", called)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+
+def _i32(*shape, device=0):
+    return OnGpu(torch.zeros(*shape, dtype=torch.int32), device)
+
+
+def _pages(rows, n_pages=5, pool_bytes=5 * PAGE):
+    pool = OnGpu(torch.zeros(pool_bytes, dtype=torch.uint8))
+    return kvq.make_pages(pool, _i32(rows, 6), n_pages, 4)
+
+
+def _calls(pages, prefix, batch=3, n_prefixes=2):
+    """Each call that follows block tables, for `batch` sequences."""
+    x = OnGpu(torch.zeros(batch, 4, 128, dtype=torch.bfloat16))
+    k = OnGpu(torch.zeros(batch, 1, 2, 128, dtype=torch.bfloat16))
+    o, s, ptrs = OnGpu(torch.zeros(batch, 4, 128)), _i32(1), OnGpu(torch.zeros(9).long())
+    lens = _i32(batch)
+    return {
+        "append": lambda: kvq.paged_quantize_append(CFG, ptrs, k, k, pages, lens, s),
+        "decode": lambda: kvq.paged_decode_attn(CFG, ptrs, pages, lens, 64, x, o, s, s),
+        "partial": lambda: kvq.paged_decode_attn_partial(CFG, ptrs, pages, lens, 64, x, o, s, s),
+        "step": lambda: kvq.paged_append_decode(CFG, ptrs, k, k, pages, lens, 64, x, o, s, s),
+        "prefix": lambda: kvq.paged_prefix_decode_attn(
+            CFG, ptrs, prefix, _i32(n_prefixes), _i32(n_prefixes + 1), 64, pages, lens, 64, x, o,
+            s, s)}
+
+
+@pytest.mark.parametrize("call", ["append", "decode", "partial", "step", "prefix"])
+def test_short_block_tables_and_pools_are_refused(call, no_call):
+    with pytest.raises(kvq.KVQError, match="pages: block table of 2 rows for 3"):
+        _calls(_pages(2), _pages(2))[call]()
+    with pytest.raises(kvq.KVQError, match="pages: pool of"):
+        _calls(_pages(3, pool_bytes=5 * PAGE - 1), _pages(2))[call]()
+    for rows in (3, 7):  # enough: the call goes through to the library
+        with pytest.raises(AssertionError, match="the library was called"):
+            _calls(_pages(rows), _pages(2))[call]()
+    # a bare description says nothing about its arrays
+    with pytest.raises(AssertionError, match="the library was called"):
+        _calls(kvq.Pages(16, 16, 5, 4, 6), kvq.Pages(16, 16, 5, 4, 6))[call]()
+
+
+def test_short_prefix_table_is_refused(no_call):
+    with pytest.raises(kvq.KVQError, match="prefix_pages: block table of 1 rows for 2"):
+        _calls(_pages(3), _pages(1))["prefix"]()
+    with pytest.raises(kvq.KVQError, match="prefix_pages: pool of"):
+        _calls(_pages(3), _pages(2, n_pages=6))["prefix"]()
+
+
+@pytest.mark.parametrize("table", [torch.zeros(3, 6, dtype=torch.int64), torch.zeros(18).int(),
+                                   torch.zeros(6, 3, dtype=torch.int32).t()])
+def test_block_table_of_another_kind_is_refused(table):
+    with pytest.raises(kvq.KVQError, match="block_table"):
+        kvq.make_pages(OnGpu(torch.zeros(5 * PAGE)), OnGpu(table), 5, 4)
+    with pytest.raises(kvq.KVQError, match="block_table"):  # host memory
+        kvq.make_pages(torch.zeros(5 * PAGE), torch.zeros(3, 6, dtype=torch.int32), 5, 4)
