@@ -346,29 +346,35 @@ def make_pages(pool, block_table, n_pages, page_tiles):
     """kvq_pages over a device pool (n_pages pages of page_bytes) and a device
     block table int32 [batch, max_pages]."""
     import torch
-    _need(block_table, "block_table", torch.int32, (block_table.shape[0], block_table.shape[-1]))
+    dev = pool.get_device()
+    _need(block_table, "block_table", torch.int32, (block_table.shape[0], block_table.shape[-1]),
+          dev)
     pages = Pages(pool.data_ptr(), block_table.data_ptr(), n_pages, page_tiles,
                   block_table.shape[1])
     # for the checks of the calls that follow the table: its rows, and the bytes
     # that the pool has for a tile's records of all KV heads
     pages.rows, pages.tile_room = block_table.shape[0], pool.nbytes // max(n_pages * page_tiles, 1)
+    pages.device = dev
     return pages
 
 
-def _pages(cfg, pages, name, rows):
-    """Refuse a block table of fewer rows than the call's sequences, or a pool
-    shorter than its pages (make_pages; a bare Pages says neither)."""
+def _pages(cfg, pages, name, rows, dev):
+    """Refuse a block table of fewer rows than the call's sequences, a pool
+    shorter than its pages, or either on another device than the call's tensors
+    (make_pages; a bare Pages says none of it)."""
     if getattr(pages, "rows", rows) < rows:
         raise KVQError(ERR_ARG, f"{name}: block table of {pages.rows} rows for {rows}")
     need = cfg.n_kv_heads * (512 * (cfg.bits_k + cfg.bits_v) + 128)
     if getattr(pages, "tile_room", need) < need:
         raise KVQError(ERR_ARG, f"{name}: pool of {pages.tile_room} bytes a tile for {need}")
+    if getattr(pages, "device", dev) != dev:
+        raise KVQError(ERR_ARG, f"{name}: on device {pages.device}, lengths on device {dev}")
 
 
 def paged_quantize_append(cfg, plan_ptrs, k, v, pages, lens, status, rope_base=0.0):
     """kvq_quantize_append into paged caches (rope_base > 1: pre-RoPE keys)."""
     batch, n_new = k.shape[0], k.shape[1]
-    _pages(cfg, pages, "pages", batch)
+    _pages(cfg, pages, "pages", batch, lens.get_device())
     _check(lib().kvq_paged_quantize_append(ctypes.byref(cfg), _ptr(plan_ptrs), _ptr(k), _ptr(v),
                                            _dtype_code(k), batch, n_new, ctypes.byref(pages),
                                            _ptr(lens), float(rope_base), _ptr(status),
@@ -378,7 +384,7 @@ def paged_quantize_append(cfg, plan_ptrs, k, v, pages, lens, status, rope_base=0
 def paged_decode_attn(cfg, plan_ptrs, pages, lens, max_len, q, out, ws, status):
     """kvq_decode_attn over paged caches."""
     batch, n_q = q.shape[0], q.shape[1]
-    _pages(cfg, pages, "pages", batch)
+    _pages(cfg, pages, "pages", batch, lens.get_device())
     _check(lib().kvq_paged_decode_attn(ctypes.byref(cfg), _ptr(plan_ptrs), ctypes.byref(pages),
                                        _ptr(lens), batch, max_len, _ptr(q), _dtype_code(q), n_q,
                                        _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
@@ -388,7 +394,7 @@ def paged_decode_attn(cfg, plan_ptrs, pages, lens, max_len, q, out, ws, status):
 def paged_decode_attn_partial(cfg, plan_ptrs, pages, lens, max_len, q, rec, ws, status):
     """kvq_decode_attn_partial over paged caches: records fp32 [batch, n_q, 132]."""
     batch, n_q = q.shape[0], q.shape[1]
-    _pages(cfg, pages, "pages", batch)
+    _pages(cfg, pages, "pages", batch, lens.get_device())
     _check(lib().kvq_paged_decode_attn_partial(ctypes.byref(cfg), _ptr(plan_ptrs),
                                                ctypes.byref(pages), _ptr(lens), batch, max_len,
                                                _ptr(q), _dtype_code(q), n_q, _ptr(rec), _ptr(ws),
@@ -401,7 +407,7 @@ def paged_append_decode(cfg, plan_ptrs, k, v, pages, lens, max_len, q, out, ws, 
     """kvq_append_decode over paged caches."""
     batch, n_q = q.shape[0], q.shape[1]
     n_new = 0 if k is None else k.shape[1]
-    _pages(cfg, pages, "pages", batch)
+    _pages(cfg, pages, "pages", batch, lens.get_device())
     _check(lib().kvq_paged_append_decode(ctypes.byref(cfg), _ptr(plan_ptrs), _ptr(k), _ptr(v),
                                          _dtype_code(k) if k is not None else BF16, n_new,
                                          ctypes.byref(pages), _ptr(lens), batch, max_len,
@@ -523,39 +529,44 @@ def _stream_of(t):
     return torch._C._cuda_getCurrentRawStream(i)
 
 
-def _need(t, name, dtype, shape):
-    """Refuse a tensor that is not a contiguous device array of this type and
-    shape: the library only sees its address. (One line of tests: the smallest
-    calls are bound by the host.)"""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise KVQError(ERR_ARG, f"{name}: contiguous {dtype} device tensor of shape "
-                                f"{tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+def _need(t, name, dtype, shape, dev):
+    """Refuse a tensor that is not a contiguous array of this type and shape on
+    device dev (not the host): the library only sees its address. (One line of
+    tests: the smallest calls are bound by the host.)"""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or dev < 0 or \
+            not t.is_contiguous():
+        raise KVQError(ERR_ARG, f"{name}: contiguous {dtype} tensor of shape {tuple(shape)} on "
+                                f"device {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _ptrs(t, name, n):
+def _ptrs(t, name, n, dev):
     """Refuse a pointer array (ptr_array) with fewer than n entries."""
-    if t.element_size() != 8 or t.numel() < n or not t.is_cuda:
-        raise KVQError(ERR_ARG, f"{name}: {t.numel()} device pointers for {n}")
+    if t.element_size() != 8 or t.numel() < n or t.get_device() != dev or dev < 0:
+        raise KVQError(ERR_ARG, f"{name}: {t.numel()} device pointers on {t.device} for {n} on "
+                                f"device {dev}")
 
 
-def _on_device(**tensors):
-    """Refuse memory that the GPU cannot address: the library only sees addresses."""
+def _on_device(dev, **tensors):
+    """Refuse memory that is not on device dev: the library only sees addresses."""
     for name, t in tensors.items():
-        if not t.is_cuda:
-            raise KVQError(ERR_ARG, f"{name}: on {t.device}, not on a GPU")
+        i = t.get_device()
+        if i != dev or i < 0:
+            raise KVQError(ERR_ARG, f"{name}: on {t.device}, not on a GPU" if i < 0 else
+                           f"{name}: on {t.device}, other tensors of the call on device {dev}")
 
 
 def make_page_state(table, held, free_ids, free_ring, page_tiles):
     """kvq_page_state over device tensors: table int32 [batch, max_pages],
     held int32 [batch], free_ids int32 [n_pages], free_ring int64 [2]."""
     import torch
-    _need(table, "table", torch.int32, (table.shape[0], table.shape[-1]))
-    _need(held, "held", torch.int32, table.shape[:1])
-    _need(free_ids, "free_ids", torch.int32, free_ids.shape[:1])
-    _need(free_ring, "free_ring", torch.int64, (2,))
+    dev = table.get_device()
+    _need(table, "table", torch.int32, (table.shape[0], table.shape[-1]), dev)
+    _need(held, "held", torch.int32, table.shape[:1], dev)
+    _need(free_ids, "free_ids", torch.int32, free_ids.shape[:1], dev)
+    _need(free_ring, "free_ring", torch.int64, (2,), dev)
     state = PageState(table.data_ptr(), held.data_ptr(), free_ids.data_ptr(),
                       free_ring.data_ptr(), free_ids.shape[0], page_tiles, table.shape[1])
-    state.rows = table.shape[0]  # for the checks of pages_assign
+    state.rows, state.device = table.shape[0], dev  # for the checks of pages_assign
     return state
 
 
@@ -568,18 +579,20 @@ def pages_assign(state, lens, n_new, cu, slots, pos, ws, status):
     Fills cu int32 [batch + 1], slots int64 [n_slots], pos int32 [n_slots] (or
     None) and moves pages between the rows and the free ring."""
     import torch
-    i32 = torch.int32
+    i32, dev = torch.int32, lens.get_device()
     batch, n_slots = lens.shape[0], slots.shape[0]
-    _need(lens, "lens", i32, (batch,))
-    _need(n_new, "n_new", i32, (batch,))
-    _need(cu, "cu", i32, (batch + 1,))
-    _need(slots, "slots", torch.int64, (n_slots,))
+    _need(lens, "lens", i32, (batch,), dev)
+    _need(n_new, "n_new", i32, (batch,), dev)
+    _need(cu, "cu", i32, (batch + 1,), dev)
+    _need(slots, "slots", torch.int64, (n_slots,), dev)
     if pos is not None:
-        _need(pos, "pos", i32, (n_slots,))
+        _need(pos, "pos", i32, (n_slots,), dev)
         pos = pos.data_ptr()
-    _on_device(ws=ws, status=status)
+    _on_device(dev=dev, ws=ws, status=status)
     if batch != getattr(state, "rows", batch):
         raise KVQError(ERR_ARG, f"{batch} sequences, block table of {state.rows} rows")
+    if dev != getattr(state, "device", dev):
+        raise KVQError(ERR_ARG, f"tensors on device {dev}, page state on device {state.device}")
     rc = lib().kvq_pages_assign(state, lens.data_ptr(), n_new.data_ptr(), batch, n_slots,
                                 cu.data_ptr(), slots.data_ptr(), pos, ws.data_ptr(), ws.nbytes,
                                 status.data_ptr(), _stream_of(lens))
@@ -592,15 +605,15 @@ def paged_append_ragged(cfg, plan_ptrs, k, v, cu, slots, pool, n_pages, page_til
     """Quantize-append the packed rows k, v [n_rows, n_kv, 128] into the slots
     of pages_assign (rope_base > 1: pre-RoPE keys) and advance lens."""
     import torch
-    batch, n_rows = lens.shape[0], k.shape[0]
+    batch, n_rows, dev = lens.shape[0], k.shape[0], lens.get_device()
     rows = (n_rows, cfg.n_kv_heads, 128)
-    _need(k, "k", k.dtype, rows)
-    _need(v, "v", k.dtype, rows)
-    _need(cu, "cu", torch.int32, (batch + 1,))
-    _need(slots, "slots", torch.int64, slots.shape[:1])
-    _need(lens, "lens", torch.int32, (batch,))
-    _on_device(pool=pool, status=status)
-    _ptrs(plan_ptrs, "plan_ptrs", batch)
+    _need(k, "k", k.dtype, rows, dev)
+    _need(v, "v", k.dtype, rows, dev)
+    _need(cu, "cu", torch.int32, (batch + 1,), dev)
+    _need(slots, "slots", torch.int64, slots.shape[:1], dev)
+    _need(lens, "lens", torch.int32, (batch,), dev)
+    _on_device(dev=dev, pool=pool, status=status)
+    _ptrs(plan_ptrs, "plan_ptrs", batch, dev)
     # a page holds page_tiles records of 512 (bits_k + bits_v) + 128 bytes per KV head
     if slots.shape[0] < n_rows or pool.nbytes < \
             n_pages * page_tiles * cfg.n_kv_heads * (512 * (cfg.bits_k + cfg.bits_v) + 128):
@@ -623,16 +636,16 @@ def prefix_decode_workspace_bytes(cfg, batch, n_q_heads, n_prefixes) -> int:
 
 def _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws, status):
     import torch
-    batch, n_prefixes = lens.shape[0], prefix_lens.shape[0]
+    batch, n_prefixes, dev = lens.shape[0], prefix_lens.shape[0], lens.get_device()
     rows = (batch, q.shape[1], 128)
-    _need(prefix_lens, "prefix_lens", torch.int32, (n_prefixes,))
-    _need(group_start, "group_start", torch.int32, (n_prefixes + 1,))
-    _need(lens, "lens", torch.int32, (batch,))
-    _need(q, "q", q.dtype, rows)
-    _need(out, "out", out.dtype, rows)
-    _ptrs(plan_ptrs, "plan_ptrs", batch)
-    _on_device(ws=ws, status=status)
-    return batch, n_prefixes
+    _need(prefix_lens, "prefix_lens", torch.int32, (n_prefixes,), dev)
+    _need(group_start, "group_start", torch.int32, (n_prefixes + 1,), dev)
+    _need(lens, "lens", torch.int32, (batch,), dev)
+    _need(q, "q", q.dtype, rows, dev)
+    _need(out, "out", out.dtype, rows, dev)
+    _ptrs(plan_ptrs, "plan_ptrs", batch, dev)
+    _on_device(dev=dev, ws=ws, status=status)
+    return batch, n_prefixes, dev
 
 
 def prefix_decode_attn(cfg, plan_ptrs, prefix_ptrs, prefix_lens, group_start, max_prefix_len,
@@ -640,10 +653,10 @@ def prefix_decode_attn(cfg, plan_ptrs, prefix_ptrs, prefix_lens, group_start, ma
     """Decode q [batch, n_q, 128] into out (bf16, fp16 or fp32) over each
     group's shared prefix cache (sequences group_start[g] .. group_start[g + 1]
     - 1 share prefix g) and each sequence's own cache."""
-    batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws,
-                                      status)
-    _ptrs(prefix_ptrs, "prefix_ptrs", n_prefixes)
-    _ptrs(cache_ptrs, "cache_ptrs", batch)
+    batch, n_prefixes, dev = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws,
+                                          status)
+    _ptrs(prefix_ptrs, "prefix_ptrs", n_prefixes, dev)
+    _ptrs(cache_ptrs, "cache_ptrs", batch, dev)
     rc = lib().kvq_prefix_decode_attn(
         cfg, plan_ptrs.data_ptr(), prefix_ptrs.data_ptr(), prefix_lens.data_ptr(),
         group_start.data_ptr(), n_prefixes, max_prefix_len, cache_ptrs.data_ptr(),
@@ -658,10 +671,10 @@ def paged_prefix_decode_attn(cfg, plan_ptrs, prefix_pages, prefix_lens, group_st
                              max_prefix_len, pages, lens, max_len, q, out, ws, status):
     """prefix_decode_attn over paged caches (the prefixes' block-table rows in
     prefix_pages, the sequences' in pages)."""
-    batch, n_prefixes = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws,
-                                      status)
-    _pages(cfg, prefix_pages, "prefix_pages", n_prefixes)
-    _pages(cfg, pages, "pages", batch)
+    batch, n_prefixes, dev = _prefix_args(plan_ptrs, prefix_lens, group_start, lens, q, out, ws,
+                                          status)
+    _pages(cfg, prefix_pages, "prefix_pages", n_prefixes, dev)
+    _pages(cfg, pages, "pages", batch, dev)
     rc = lib().kvq_paged_prefix_decode_attn(
         cfg, plan_ptrs.data_ptr(), prefix_pages, prefix_lens.data_ptr(), group_start.data_ptr(),
         n_prefixes, max_prefix_len, pages, lens.data_ptr(), batch, max_len, q.data_ptr(),

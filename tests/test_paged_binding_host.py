@@ -84,3 +84,89 @@ def test_block_table_of_another_kind_is_refused(table):
         kvq.make_pages(OnGpu(torch.zeros(5 * PAGE)), OnGpu(table), 5, 4)
     with pytest.raises(kvq.KVQError, match="block_table"):  # host memory
         kvq.make_pages(torch.zeros(5 * PAGE), torch.zeros(3, 6, dtype=torch.int32), 5, 4)
+
+
+def _arguments(device):
+    """Every tensor of the paged-serving calls, on one device."""
+    def on(t):
+        return OnGpu(t, device)
+    ptrs = torch.zeros(9).long()
+    return dict(
+        lens=_i32(3, device=device), n_new=_i32(3, device=device), cu=_i32(4, device=device),
+        slots=on(torch.zeros(5).long()), pos=_i32(5, device=device), ws=_i32(64, device=device),
+        status=_i32(1, device=device), table=_i32(3, 6, device=device),
+        held=_i32(3, device=device), free_ids=_i32(5, device=device),
+        free_ring=on(torch.zeros(2).long()), plan_ptrs=on(ptrs), prefix_ptrs=on(ptrs),
+        cache_ptrs=on(ptrs), k=on(torch.zeros(5, 2, 128)), v=on(torch.zeros(5, 2, 128)),
+        pool=on(torch.zeros(5 * PAGE, dtype=torch.uint8)), prefix_lens=_i32(2, device=device),
+        group_start=_i32(3, device=device), q=on(torch.zeros(3, 4, 128)),
+        out=on(torch.zeros(3, 4, 128)), prefix_table=_i32(2, 6, device=device))
+
+
+def _assign(a):
+    state = kvq.make_page_state(a["table"], a["held"], a["free_ids"], a["free_ring"], 4)
+    kvq.pages_assign(state, a["lens"], a["n_new"], a["cu"], a["slots"], a["pos"], a["ws"],
+                     a["status"])
+
+
+def _append(a):
+    kvq.paged_append_ragged(CFG, a["plan_ptrs"], a["k"], a["v"], a["cu"], a["slots"], a["pool"], 5,
+                            4, a["lens"], a["status"])
+
+
+def _prefix(a):
+    kvq.prefix_decode_attn(CFG, a["plan_ptrs"], a["prefix_ptrs"], a["prefix_lens"],
+                           a["group_start"], 64, a["cache_ptrs"], a["lens"], 64, a["q"], a["out"],
+                           a["ws"], a["status"])
+
+
+def _paged_prefix(a):
+    kvq.paged_prefix_decode_attn(
+        CFG, a["plan_ptrs"], kvq.make_pages(a["pool"], a["prefix_table"], 5, 4), a["prefix_lens"],
+        a["group_start"], 64, kvq.make_pages(a["pool"], a["table"], 5, 4), a["lens"], 64, a["q"],
+        a["out"], a["ws"], a["status"])
+
+
+_SHARED = "plan_ptrs prefix_lens group_start lens q out ws status"
+_TENSORS = {_assign: "lens n_new cu slots pos ws status table held free_ids free_ring",
+            _append: "plan_ptrs k v cu slots pool lens status",
+            _prefix: _SHARED + " prefix_ptrs cache_ptrs",
+            _paged_prefix: _SHARED + " pool table prefix_table"}
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, names in _TENSORS.items()
+                                       for n in names.split()])
+def test_a_tensor_on_another_gpu_is_refused(call, name, no_call):
+    """The library launches on the current device and takes addresses alone."""
+    args = _arguments(0)
+    with pytest.raises(AssertionError, match="the library was called"):
+        call(args)
+    args[name] = _arguments(1)[name]
+    with pytest.raises(kvq.KVQError):
+        call(args)
+
+
+@pytest.mark.parametrize("call", list(_TENSORS))
+def test_all_tensors_on_another_gpu_than_the_current_one(call, monkeypatch):
+    class Lib:  # the stream is asked for before the entry point is called
+        def __getattr__(self, name):
+            def entry(*args):
+                raise AssertionError("the library was called")
+            return entry
+    monkeypatch.setattr(kvq, "lib", Lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(kvq.KVQError, match="current device 0"):
+        call(_arguments(1))
+
+
+def test_all_page_state_on_another_gpu_is_refused(no_call):
+    args = _arguments(0)
+    for name in ("table", "held", "free_ids", "free_ring"):
+        args[name] = _arguments(1)[name]
+    with pytest.raises(kvq.KVQError, match="page state on device 1"):
+        _assign(args)
+    args = _arguments(0)
+    for name in ("pool", "table", "prefix_table"):
+        args[name] = _arguments(1)[name]
+    with pytest.raises(kvq.KVQError, match="on device 1, lengths on device 0"):
+        _paged_prefix(args)
