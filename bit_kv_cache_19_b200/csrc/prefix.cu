@@ -111,7 +111,10 @@ static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // type, and the layout covers both (units: the 128-row count; record rows: 256).
 static PfxLayout pfx_layout(int batch, int n_q, int n_kv, int n_groups, int n_ctas) {
   const int G = n_q / n_kv;
-  const size_t units = (size_t)n_kv * (n_groups + ((size_t)batch * G + 127) / 128);
+  // a group without sequences has no unit, and no more groups have any than there
+  // are sequences
+  const size_t units =
+      (size_t)n_kv * (std::min(n_groups, batch) + ((size_t)batch * G + 127) / 128);
   // incidences of (CTA, unit): one per step of a staircase
   const size_t inc_p = units + n_ctas, inc_s = (size_t)batch * n_kv + n_ctas;
   PfxLayout w;
