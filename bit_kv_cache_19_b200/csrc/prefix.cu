@@ -167,7 +167,9 @@ struct PrefixParams {
 __device__ __forceinline__ int clamp_len(int32_t l, int64_t most) {
   return (int)min((int64_t)max(l, 0), most);
 }
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTok - 1) / kTok; }
+// tiles and records of a length up to 2^31 - 1
+__device__ __forceinline__ int tiles_of(int len) { return len / kTok + (len % kTok != 0); }
+__device__ __forceinline__ int recs_of(int len) { return len / kTile + (len % kTile != 0); }
 
 // Cost line of one group: n_kv blocks of nrt units, the last of `last` rows.
 struct GroupCost {
@@ -850,7 +852,7 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
       if (more) u = next_unit(p, u, suffix0, lane);
       continue;
     }
-    const int row = u.suffix ? u.b : u.g, n_rec = (u.len + kTile - 1) / kTile;
+    const int row = u.suffix ? u.b : u.g, n_rec = recs_of(u.len);
     const Plan* const plan = p.a.plans[u.b] + u.h;
     unsigned long long base = 0;
     if (4 * t0 + lane < n_rec)
@@ -951,7 +953,7 @@ __device__ __forceinline__ void copy_role(const PrefixParams& p, MainSmem& sm, u
     ok = wait_warp(sm, &sm.desc_ready[ds], (seg / kDescs) & 1);
     const Desc& d = sm.desc[ds];
     if (!ok || d.stop) break;
-    const int tiles = d.tiles, n_rec = (d.len + kTile - 1) / kTile, row = d.row, h = d.h;
+    const int tiles = d.tiles, n_rec = recs_of(d.len), row = d.row, h = d.h;
     const int rec0 = 4 * d.tile0;
     const bool suffix = d.suffix;
     const int mask = suffix ? page_mask(p.a.own) : page_mask(p.a.pre);
@@ -1029,7 +1031,7 @@ __device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm,
     const KeyStep k0 = key_step(pl, uw < n_half ? uw : 0, lane);
     const KeyStep k1 = key_step(pl, hs1 < n_half ? hs1 : 0, lane);
     const int n_steps = (uw < n_half) + (hs1 < n_half);
-    const int n_rec = (d.len + kTile - 1) / kTile, key_bytes = 512 * p.a.bits_k;
+    const int n_rec = recs_of(d.len), key_bytes = 512 * p.a.bits_k;
     const int norm_off = key_bytes + 512 * BV;
     const int me = uw >= 3 && uw < 7 ? uw - 3 : 4;  // a record's norms, or none
     const int tiles = d.tiles, tile0 = d.tile0, len = d.len;

@@ -1,11 +1,15 @@
 """GPU: the shared-prefix decode at the ends of what its interface allows: more
-prefixes than sequences, in a workspace of exactly the size asked for."""
+prefixes than sequences in a workspace of exactly the size asked for, and the longest
+context."""
 import numpy as np
 import pytest
 import torch
 
+import synth
 from bit_kv_cache_19_b200 import kvq
-from test_gpu_prefix_decode import DEV, Setup, check, contiguous, group_of, reference
+from bit_kv_cache_19_b200.runtime import DevicePageAllocator, PagedLayer, prefix_workspace
+from test_gpu_prefix_decode import (DEV, Setup, check, contiguous, dev_bf16, group_of,
+                                    reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +48,40 @@ def test_many_empty_prefixes_in_an_exact_workspace(dtype):
     ref, tol = reference(S, q.double().numpy(), heads, [S.heads(*x) for x in od],
                          group_of(start, 5), dtype)
     check(out, ref, tol)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_longest_context(shared):
+    """2^31 - 32 tokens, the most a block table holds: every entry is the same page of 32
+    tokens, so the output is the mean of its 32 values (q = 0: all weights are one power
+    of two). Bound on the error's norm relative to the mean of the values' norms: a stream
+    of the at least 100 CTAs adds at most 2^31 / 100 / 2 / 16 products of 16 tokens to one
+    fp32 sum (the sums of the weights stay exact below 2^24 units), each addition good to
+    2^-23: 2^-23 * 671089 = 0.08. What the test is for is that the tokens are there at
+    all: the values share a mean near their norm."""
+    S = Setup(53, 1, 1, 1)
+    n, wide = (1 << 31) - 32, (1 << 26) - 1
+    kb, vb = S.tokens(32)
+    base = S.rng.standard_normal(128)
+    vb = synth.to_bf16_bits(base + 0.1 * S.rng.standard_normal((32, 1, 128)))
+    P = PagedLayer(S.cfg, 1, 1, 1, 1, layer=1, pages=DevicePageAllocator(1, 1, 1, 1))
+    P.set_plans(S.plans)
+    cu, slots, _ = P.assign(torch.tensor([32], dtype=torch.int32, device=DEV), 32)
+    P.append_ragged(dev_bf16(kb), dev_bf16(vb), cu, slots)
+    table = torch.zeros(1, wide, dtype=torch.int32, device=DEV)
+    long, none = kvq.make_pages(P.pool, table, 1, 1), kvq.make_pages(P.pool, table[:, :1], 1, 1)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    zero, gs = torch.zeros_like(lens), torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    q = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    ws = prefix_workspace(S.cfg, 1, 2, 1)
+    args = (long, lens, gs, n, none, zero) if shared else (none, zero, gs, 32, long, lens)
+    kvq.paged_prefix_decode_attn(S.cfg, P.plan_ptrs, *args, 32 if shared else n, q, out, ws,
+                                 P.status)
+    assert P.flags() == 0
+    v = S.heads(kb, vb)[0][1]
+    ref, size = v.mean(axis=0), np.linalg.norm(v, axis=1).mean()
+    assert np.linalg.norm(ref) > 0.5 * size
+    for h in range(2):
+        err = np.linalg.norm(out[0, h].double().cpu().numpy() - ref)
+        assert err <= 0.08 * size + 2.0 ** -8 * np.linalg.norm(ref), err / size
