@@ -162,6 +162,7 @@ struct PrefixParams {
   float2 *ml_p, *ml_s;
   float *o_p, *o_s;
   int ring;  // tile slots (4 records each)
+  long long stall_cycles;  // test hook (> 0): the products stop after so long a wait
 };
 
 __device__ __forceinline__ int clamp_len(int32_t l, int64_t most) {
@@ -574,6 +575,7 @@ struct alignas(128) MainSmem {
   unsigned long long ring_full[kMaxRing], ring_empty[kMaxRing];
   unsigned long long q_full[2], q_empty[2], k_full[2], k_empty[2], v_full, v_empty;
   unsigned long long s_full[2], p_ready[2], o_full[2], o_free[2], lut_full, drain;
+  unsigned long long stall;  // nothing arrives on it
   uint32_t tmem;
   int fail;
 };
@@ -932,12 +934,12 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
       mbar_arrive(&sm.desc_full[ds]);
     }
   }
-  if (!ok) {  // let the copies in flight land before the CTA ends
-    if (quse[0]) (void)mbar_wait_bounded(&sm.q_full[0], (quse[0] - 1) & 1);
-    if (quse[1]) (void)mbar_wait_bounded(&sm.q_full[1], (quse[1] - 1) & 1);
-    for (uint32_t i = 1; i <= kDescs && i <= seg; ++i)
-      (void)mbar_wait_bounded(&sm.desc_full[(seg - i) % kDescs], ((seg - i) / kDescs) & 1);
-  }
+  // the copies land before the CTA ends, also when their readers have given up (the
+  // end's descriptor took the slot of the fourth last segment, whose readers are done)
+  if (quse[0]) (void)mbar_wait_bounded(&sm.q_full[0], (quse[0] - 1) & 1);
+  if (quse[1]) (void)mbar_wait_bounded(&sm.q_full[1], (quse[1] - 1) & 1);
+  for (uint32_t i = 1; i <= (ok ? kDescs - 1 : kDescs) && i <= seg; ++i)
+    (void)mbar_wait_bounded(&sm.desc_full[(seg - i) % kDescs], ((seg - i) / kDescs) & 1);
 }
 
 // Streams the segments' records into the ring, a tile (up to four records, one
@@ -997,10 +999,10 @@ __device__ __forceinline__ void copy_role(const PrefixParams& p, MainSmem& sm, u
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.desc_empty[ds]);
   }
-  if (!ok)  // let the copies in flight land before the CTA ends: the last use of
-            // each slot had the ring's phase, or the one before
-    for (uint32_t i = 0; i < issued; ++i)
-      (void)mbar_wait_bounded(&sm.ring_full[i], i < rp.slot ? rp.phase : rp.phase ^ 1);
+  // the copies land before the CTA ends, also when their readers have given up: the
+  // last use of each slot had the ring's phase, or the one before
+  for (uint32_t i = 0; i < issued; ++i)
+    (void)mbar_wait_bounded(&sm.ring_full[i], i < rp.slot ? rp.phase : rp.phase ^ 1);
 }
 
 template <int BV>
@@ -1014,7 +1016,11 @@ __device__ __forceinline__ void unpack_role(const PrefixParams& p, MainSmem& sm,
   // V tile
   const int lag = n_ring > 1 ? 1 : 0;
   const uint32_t tbytes = p.tile_bytes;
-  if (!wait_warp(sm, &sm.lut_full, 0)) return;
+  // not cut short when another role gives up: the copy must land before the CTA ends
+  if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sm.lut_full, 0))) {
+    *(volatile int*)&sm.fail = 1;
+    return;
+  }
   for (;; ++seg) {
     const uint32_t ds = seg % kDescs;
     if (!wait_warp(sm, &sm.desc_full[ds], (seg / kDescs) & 1)) return;
@@ -1130,6 +1136,11 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
 #pragma unroll 1
   for (uint32_t k = 0, issued = 0, done = 0;; ++k) {
     const int s = k & 1;
+    if (p.stall_cycles > 0 && k == (blockIdx.x & 7)) {  // test hook: a wait that runs out
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sm.stall, 0, p.stall_cycles)))
+        *(volatile int*)&sm.fail = 1;
+      return;
+    }
     if (k >= 2 && done < issued) {
       if (v.j == v.n) {  // the next segment's values
         if (v.n) {
@@ -1491,6 +1502,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
     mbar_init(&sm.v_empty, 1);
     mbar_init(&sm.lut_full, 1);
     mbar_init(&sm.drain, 1);
+    mbar_init(&sm.stall, 1);
     sm.fail = 0;
     fence_proxy_async();
     mbar_expect_tx(&sm.lut_full, KVQ_LUT_BYTES);
@@ -1767,6 +1779,7 @@ cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes,
   p.G = a.n_q / a.n_kv;
   p.tile_bytes = tile_bytes(a.bits_k, a.bits_v);
   p.rows_unit = split ? 128 : 256;
+  p.stall_cycles = decode_stall();
   uint8_t* const s = static_cast<uint8_t*>(ws);
   p.head = reinterpret_cast<PfxHead*>(s + w.head);
   p.cuts = reinterpret_cast<int64_t*>(s + w.cuts);

@@ -422,7 +422,9 @@ KVQ_API int kvq_combine_partials(const kvq_cfg* cfg, const void* const* plans_de
  * arrives on. The wait runs out, the launch sets KVQ_FLAG_TIMEOUT in
  * *status_dev, lets the tile copies it already issued land, skips its tiles
  * and completes normally (its outputs are then meaningless), which exercises
- * the path every bounded wait of the kernels takes when it gives up. 0
+ * the path every bounded wait of the kernels takes when it gives up. In
+ * kvq_prefix_decode_attn the warp that issues the products waits so, some steps
+ * in, and leaves; every other role then gives up at its next wait. 0
  * restores normal launches. Process-wide; for tests only. Returns KVQ_OK or
  * KVQ_ERR_ARG.
  */
