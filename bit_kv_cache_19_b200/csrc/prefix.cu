@@ -16,9 +16,21 @@
 // log2(e) / sqrt(128) scaled by a power of two per row; the token's key norm
 // multiplies the fp32 logit. V = the centroids of the rotated values, P =
 // 2^(s - m) times the value norm, in fp16. The inverse rotation comes after
-// the merge. Rounding: for bf16 outputs Q and P are rounded to fp16 once (2^-11
-// relative at most each, an eighth of the output's own 2^-8); for fp16 and fp32
-// outputs both are split into two fp16 terms (hi + lo), two products each.
+// the merge. Rounding: a query row is a pair of fp16 terms (hi + lo, 22 bits, two
+// products); P is one term for bf16 outputs (2^-11 of each weight, an eighth of the
+// output's own 2^-8) and a pair for fp16 and fp32. Only a unit of more than 128 rows,
+// whose second row tile takes the low parts' room, has one term per query element: for
+// bf16 queries with bf16 outputs alone. 2^-11, an eighth of what a bf16 query element
+// carries already, is then relative to each product q_i k_i, so a weight is off by up
+// to 2^-11 sum |q_i k_i| / sqrt(128) of itself. Measured against 64 bits, relative to
+// the norm: 2.2e-3 for 64 sequences behind 131072 tokens (512 rows), of which the
+// output's own rounding is 1.7e-3; pairs there would unpack the prefix twice as often.
+// With pairs (28 query rows on 4 KV heads, 16 sequences) 1.65e-3, 1.64e-3 of it the
+// output's; one term had 1.71e-3 and 35.3 us instead of 36.1, and for 48 sequences
+// behind three documents 59.5 instead of 61.3.
+// O is summed in tensor memory in fp32, which drops what falls below its last bit:
+// about 2^-24 of O per 16 tokens of one CTA's piece (fp32 outputs: 1e-6 of the norm for
+// 2048 tokens, 1.2e-5 for 64 sequences behind 131072; eager fp32: 8e-7, 8.5e-6).
 //
 // Three launches (programmatic dependent launch between them):
 //  1. prep: query rows into fp16 operand images (swizzled), the work schedule;
@@ -64,6 +76,11 @@ constexpr uint32_t kTileBytes = 2 * kPanel;
 constexpr uint32_t kQImage = 2 * kTileBytes;      // one unit's query image
 constexpr int kSufRows = 16;                      // rows of a sequence's query image
 constexpr uint32_t kSufImage = 2 * 2 * kSufRows * 128;  // 2 panels, hi and lo
+// A query slot (one tile) holds up to 64 rows as high and low parts, the low ones
+// from row 64 on; more rows take both slots, for the two parts or, above 128, for
+// the two row tiles
+constexpr int kSlotRows = 64;
+constexpr uint32_t kSlotLow = kSlotRows * 128;
 constexpr int kMaxRing = 8;  // tiles in flight
 constexpr int kNormSlots = 4;
 // TMEM columns
@@ -107,8 +124,8 @@ struct PfxLayout {
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// n_ctas bounds the main grid; rows per prefix unit are 256 or 128 by output
-// type, and the layout covers both (units: the 128-row count; record rows: 256).
+// n_ctas bounds the main grid; rows per prefix unit are 256 or 128 by the types,
+// and the layout covers both (units: the 128-row count; record rows: 256).
 static PfxLayout pfx_layout(int batch, int n_q, int n_kv, int n_groups, int n_ctas) {
   const int G = n_q / n_kv;
   // a group without sequences has no unit, and no more groups have any than there
@@ -409,8 +426,7 @@ __device__ __forceinline__ void prep_schedule(const PrefixParams& p, PrepSmem& s
 }
 
 // One query row (a warp) as fp16 operand row `row` of the image at img (panel
-// stride `panel`), its low part `lo` bytes on; isc gets 2^-sigma.
-template <bool SPLIT>
+// stride `panel`), its low part `lo` bytes on (0: none); isc gets 2^-sigma.
 __device__ __forceinline__ void prep_row(const PrefixParams& p, const PrepSmem& sm, bool plan_ok,
                                          float* buf, int b, int head, uint8_t* img, uint32_t lo,
                                          uint32_t panel, int row, float* isc, int lane) {
@@ -452,7 +468,7 @@ __device__ __forceinline__ void prep_row(const PrefixParams& p, const PrepSmem& 
     const uint32_t at = i * panel + row * 128 + ((((uint32_t)lane >> 2) ^ (row & 7)) << 4) +
                         (lane & 3) * 4;
     *reinterpret_cast<uint32_t*>(img + at) = hi;
-    if constexpr (SPLIT) {
+    if (lo) {
       const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
       *reinterpret_cast<uint32_t*>(img + lo + at) =
           pack_half2(x0 - __low2float(hh), x1 - __high2float(hh));
@@ -475,7 +491,6 @@ __device__ __forceinline__ bool load_plan(const PrefixParams& p, PrepSmem& sm, c
   return ok;
 }
 
-template <bool SPLIT>
 __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixParams p) {
   __shared__ PrepSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -543,12 +558,12 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixP
       uint32_t lo = kSufImage / 2;
       if (part) {
         img = p.q_p + (size_t)(sm.gunit[g] + h * nrt + rt) * kQImage;
-        lo = kTileBytes;
-        if (!SPLIT) img += (r >> 7) * kTileBytes;
+        img += (r >> 7) * kTileBytes;
+        lo = min(rows - rt * p.rows_unit, p.rows_unit) > 128 ? 0 : kTileBytes;
       }
-      prep_row<SPLIT>(p, sm, ok, sm.row[warp], b, h * p.G + i, img, lo,
-                      part ? kPanel : kSufRows * 128, part ? r & 127 : i,
-                      (part ? p.isc_p : p.isc_s) + (size_t)b * p.a.n_q + h * p.G + i, lane);
+      prep_row(p, sm, ok, sm.row[warp], b, h * p.G + i, img, lo,
+               part ? kPanel : kSufRows * 128, part ? r & 127 : i,
+               (part ? p.isc_p : p.isc_s) + (size_t)b * p.a.n_q + h * p.G + i, lane);
     }
   }
 }
@@ -832,7 +847,6 @@ __device__ __forceinline__ Unit next_unit(const PrefixParams& p, const Unit& u, 
 
 // Walks the CTA's piece of the cost line: one descriptor, plan and query image
 // per segment, ahead of the other roles.
-template <bool SPLIT>
 __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, uint8_t* qbuf,
                                           int lane) {
   const int64_t suffix0 = p.head->suffix0;
@@ -863,7 +877,7 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
     const uint32_t ds = seg % kDescs;
     ok = wait_warp(sm, &sm.desc_empty[ds], ((seg / kDescs) & 1) ^ 1);
     if (!ok) break;
-    const bool both = u.shared || SPLIT;
+    const bool both = u.rows > kSlotRows;
     const int qs = both ? 0 : qnext;
     Desc& d = sm.desc[ds];
     d.base[lane] = base;
@@ -895,24 +909,27 @@ __device__ __forceinline__ void walk_role(const PrefixParams& p, MainSmem& sm, u
     ++seg;
     items += (t1 - t0) << (u.shared ? 1 : 0);
 #pragma unroll 1
-    for (int i = 0; i < (both ? 2 : 1); ++i) {
-      const int s = qs + i;
-      ok = wait_warp(sm, &sm.q_empty[s], (quse[0] * (s == 0) + quse[1] * (s == 1)) & 1 ^ 1);
-      if (!ok) break;
-      // rows of this slot: the row tile of stream i, or all rows (hi, lo)
+    for (int i = 0; i < 2; ++i) {
+      const int s = both ? i : qs;
+      if (both || i == 0) {
+        ok = wait_warp(sm, &sm.q_empty[s], (quse[0] * (s == 0) + quse[1] * (s == 1)) & 1 ^ 1);
+        if (!ok) break;
+        quse[0] += s == 0;
+        quse[1] += s == 1;
+      }
+      // the row tile of stream i, or the high or low parts of all rows
       const int rows = u.shared ? min(128, u.rows - 128 * i) : u.rows;
       const uint32_t bytes = (uint32_t)(rows + 7) / 8 * 1024;
       if (lane == 0) {
         const uint8_t* src = u.suffix ? p.q_s + (size_t)u.idx * kSufImage + i * (kSufImage / 2)
                                       : p.q_p + (size_t)u.idx * kQImage + i * kTileBytes;
         const uint32_t panel = u.suffix ? kSufRows * 128 : kPanel;
-        mbar_expect_tx(&sm.q_full[s], 2 * bytes);
-        bulk_g2s(qbuf + s * kTileBytes, src, bytes, &sm.q_full[s]);
-        bulk_g2s(qbuf + s * kTileBytes + kPanel, src + panel, bytes, &sm.q_full[s]);
+        uint8_t* const dst = qbuf + s * kTileBytes + (both ? 0 : i * kSlotLow);
+        if (both || i == 0) mbar_expect_tx(&sm.q_full[s], (both ? 2 : 4) * bytes);
+        bulk_g2s(dst, src, bytes, &sm.q_full[s]);
+        bulk_g2s(dst + kPanel, src + panel, bytes, &sm.q_full[s]);
       }
       __syncwarp();
-      quse[0] += s == 0;
-      quse[1] += s == 1;
     }
     if (!both) qnext ^= 1;
     if (t0 == 0) {  // the unit starts here: where its pieces lie, for the merge
@@ -1132,6 +1149,7 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
   ItemCursor q{0u, 0u, 0u, 0u, false}, v{0u, 0u, 0u, 0u, false};
   uint32_t ksteps = 0;
   int q0 = 0;
+  bool both = false;  // the segment's queries are in both slots
   bool more = true;
 #pragma unroll 1
   for (uint32_t k = 0, issued = 0, done = 0;; ++k) {
@@ -1187,9 +1205,10 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
       if (more) {
         q.load(d);
         q0 = d.qslot;
+        both = d.rows > kSlotRows;
         ksteps = (min(max(d.plan.n_ranks, 1), 64) + 7) / 8;
 #pragma unroll 1
-        for (int i = q0; i < q0 + (q.shared || SPLIT ? 2 : 1); ++i) {
+        for (int i = q0; i < q0 + (both ? 2 : 1); ++i) {
           if (!wait_warp(sm, &sm.q_full[i], quse >> i & 1)) return;
           quse ^= 1u << i;
         }
@@ -1203,8 +1222,9 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
       if (elected) {
         const uint32_t d = tmem + kColS + 128 * s, kt = kd + st * kTileD;
 #pragma unroll 1
-        for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-          const uint32_t a = qd + (SPLIT ? part : q0 + (q.shared ? q.j & 1 : 0)) * kTileD;
+        for (int part = 0; part < (q.shared ? 1 : 2); ++part) {
+          const uint32_t a = qd + (both ? (q.shared ? q.j & 1 : part) * kTileD
+                                        : q0 * kTileD + part * (kSlotLow >> 4));
           if (part == 0) mma_ss<false>(d, a, kt, kIdesc);
           else mma_ss<true>(d, a, kt, kIdesc);
 #pragma unroll
@@ -1218,7 +1238,7 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
         if (q.last_use()) mma_commit(&sm.k_empty[st]);
         if (q.j + 1 == q.n) {  // the segment's query rows are no longer needed
           mma_commit(&sm.q_empty[q0]);
-          if (q.shared || SPLIT) mma_commit(&sm.q_empty[q0 + 1]);
+          if (both) mma_commit(&sm.q_empty[1]);
         }
       }
       __syncwarp();
@@ -1528,7 +1548,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefix_main_kernel(const PrefixP
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kWalkWarp) {
-      walk_role<SPLIT>(p, sm, qbuf, lane);
+      walk_role(p, sm, qbuf, lane);
     } else if (warp == kCopyWarp) {
       copy_role(p, sm, ring, lane);
     } else if (warp == kMmaWarp) {
@@ -1745,7 +1765,7 @@ static cudaError_t launch_main(const PrefixParams& p, cudaStream_t st) {
 template <bool SPLIT>
 static cudaError_t launch_all(const PrefixParams& p, cudaStream_t st) {
   cudaError_t e =
-      launch_pdl(st, prefix_prep_kernel<SPLIT>, 1 + p.a.batch * p.a.n_kv, kPrepThreads, 0, p);
+      launch_pdl(st, prefix_prep_kernel, 1 + p.a.batch * p.a.n_kv, kPrepThreads, 0, p);
   if (e != cudaSuccess) return e;
   switch (p.a.bits_v) {
     case 1: e = launch_main<1, SPLIT>(p, st); break;
@@ -1778,7 +1798,9 @@ cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes,
   const bool split = a.out_dtype != KVQ_BF16;
   p.G = a.n_q / a.n_kv;
   p.tile_bytes = tile_bytes(a.bits_k, a.bits_v);
-  p.rows_unit = split ? 128 : 256;
+  // a query operand of two terms leaves no room for a second row tile: 256 rows to a
+  // unit only where the queries come with bf16's 8 bits (see the top of the file)
+  p.rows_unit = split || a.q_dtype != KVQ_BF16 ? 128 : 256;
   p.stall_cycles = decode_stall();
   uint8_t* const s = static_cast<uint8_t*>(ws);
   p.head = reinterpret_cast<PfxHead*>(s + w.head);

@@ -178,7 +178,8 @@ class PackedLayer:
         """q [batch, n_q, 128] over shared prefixes, then each sequence's own
         tokens: sequences group_start[g] .. group_start[g + 1] - 1 (int32, device)
         share sequence g of ``prefix``, another PackedLayer with the same plans.
-        out: q's type unless given (bf16, fp16 or fp32)."""
+        out: q's type unless given (bf16, fp16 or fp32); decode gives fp32, which
+        is the most precise form here too."""
         _same_format(self, prefix)
         if out is None:
             out = torch.empty_like(q)
@@ -415,7 +416,8 @@ class PagedLayer:
         """q [batch, n_q, 128] over shared prefixes, then each sequence's own
         tokens: sequences group_start[g] .. group_start[g + 1] - 1 (int32, device)
         share row g of ``prefix``, another PagedLayer with the same plans. out:
-        q's type unless given (bf16, fp16 or fp32)."""
+        q's type unless given (bf16, fp16 or fp32); decode gives fp32, which is
+        the most precise form here too."""
         _same_format(self, prefix)
         if out is None:
             out = torch.empty_like(q)

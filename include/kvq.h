@@ -717,8 +717,9 @@ KVQ_API int kvq_paged_append_ragged(const kvq_cfg* cfg, const void* const* plans
  * attends over the tokens of prefix g followed by its own,
  *   o_h = sum_t softmax_t(q_h . k_hat_t / sqrt(128)) v_hat_t
  * over both, k_hat and v_hat as for kvq_decode_attn. A prefix is unpacked once
- * for up to 256 query rows (sequences x query heads of a KV head) on the tensor
- * cores, so its cost does not grow with each sequence that shares it.
+ * for up to 256 query rows (sequences x query heads of a KV head; 128 unless
+ * queries and outputs are KVQ_BF16) on the tensor cores, so its cost does not
+ * grow with each sequence that shares it.
  * prefix caches: n_prefixes caches (kvq_prefix_decode_attn) or block-table rows
  *        (kvq_paged_prefix_decode_attn; same pool as the sequences or another),
  *        prefix_len_dev int32 [n_prefixes], each <= max_prefix_len.
@@ -733,10 +734,16 @@ KVQ_API int kvq_paged_append_ragged(const kvq_cfg* cfg, const void* const* plans
  *        bound are clamped and flag CAPACITY.
  * q_dev: [batch][n_q_heads][128] of q_dtype (post-RoPE, at each sequence's full
  *        position); out_dev: the same shape of out_dtype (KVQ_BF16, KVQ_FP16 or
- *        KVQ_FP32), 16-byte aligned. For KVQ_BF16 the scaled query rows and the
- *        attention weights enter the products rounded to fp16 (relative 2^-11
- *        at most); for KVQ_FP16 and KVQ_FP32 as pairs of fp16 terms (about 22
- *        bits), so an fp32 output is good to about 1e-6 of its norm.
+ *        KVQ_FP32), 16-byte aligned. Query rows enter the products as pairs of fp16
+ *        terms (22 bits), attention weights so for KVQ_FP16 and KVQ_FP32 outputs,
+ *        rounded to fp16 once (2^-11) for KVQ_BF16. Where KVQ_BF16 queries and
+ *        outputs have more than 128 rows (sequences of a group x query heads of a
+ *        KV head), the rows are rounded to fp16 once too: 2^-11 of each element, an
+ *        eighth of a bf16 element's own rounding; a weight may then be off by 2^-11
+ *        sum |q_i k_i| / sqrt(128) of itself. Ask for KVQ_FP32 outputs where that
+ *        matters. An fp32 output is good to about 1e-6 of its norm for contexts of
+ *        some thousand tokens; sums over long ones lose up to 2^-23 per 16 tokens
+ *        that one CTA adds up (1.2e-5 measured for 64 sequences behind 131072).
  * ws_dev: >= kvq_prefix_decode_workspace_bytes(...) bytes, 256-byte aligned;
  *        contents overwritten, no initial value; calls that overlap on the GPU
  *        need workspaces of their own.
