@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixP
       sign[i] = sm.plan.v_sign[i];
     }
     if (!same && tid == 0) atomicOr(p.a.status, KVQ_FLAG_BAD_PLAN);
-    const int rows = (sm.gstart[g + 1] - sm.gstart[g]) * p.G;
+    const int rows = part ? (sm.gstart[g + 1] - sm.gstart[g]) * p.G : 0;
     const int nrt = (rows + p.rows_unit - 1) / p.rows_unit;
 #pragma unroll 1
     for (int i = warp; i < p.G; i += kPrepThreads / 32) {

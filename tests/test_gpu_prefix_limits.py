@@ -14,20 +14,22 @@ from test_gpu_prefix_decode import (DEV, Setup, check, contiguous, dev_bf16, gro
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("end", [5, 4])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_many_empty_prefixes_in_an_exact_workspace(dtype):
+def test_many_empty_prefixes_in_an_exact_workspace(dtype, end):
     """1024 prefixes, of which five sequences use three: nothing is written past the
-    workspace, which does not grow with the prefixes that no sequence has."""
+    workspace, which does not grow with the prefixes that no sequence has. end: with 4
+    the last sequence lies behind every group."""
     S = Setup(51, 2, 3, 3)
     n_prefixes, own = 1024, [3, 40, 0, 70, 33]
     used = {7: 100, 500: 257, 1023: 31}  # prefix: tokens
     lens = [used.get(g, 0) for g in range(n_prefixes)]
-    edge = {7: (0, 1), 500: (1, 3), 1023: (3, 5)}
+    edge = {7: (0, 1), 500: (1, 3), 1023: (3, end)}
     start, at = [], 0
     for g in range(n_prefixes):
         start.append(edge[g][0] if g in edge else at)
         at = edge[g][1] if g in edge else at
-    start.append(5)
+    start.append(end)
     pd = {g: S.tokens(n) for g, n in used.items()}
     od = [S.tokens(n) for n in own]
     none = ([], [])
