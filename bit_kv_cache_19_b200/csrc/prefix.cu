@@ -28,9 +28,13 @@
 // With pairs (28 query rows on 4 KV heads, 16 sequences) 1.65e-3, 1.64e-3 of it the
 // output's; one term had 1.71e-3 and 35.3 us instead of 36.1, and for 48 sequences
 // behind three documents 59.5 instead of 61.3.
-// O is summed in tensor memory in fp32, which drops what falls below its last bit:
-// about 2^-24 of O per 16 tokens of one CTA's piece (fp32 outputs: 1e-6 of the norm for
-// 2048 tokens, 1.2e-5 for 64 sequences behind 131072; eager fp32: 8e-7, 8.5e-6).
+// Sums in tensor memory are fp32 and drop what falls below their last bit at every
+// step of 16 terms. A logit's products are therefore issued from the small ones to the
+// large: low parts first, then the blocks by energy (the other way round a logit lost
+// 7e-7 of itself, now 1e-7; 257 tokens, fp32 outputs: 4.8e-7 to 1.2e-6 of the norm,
+// now 4e-7 to 5e-7). O loses up to 2^-23 per 16 tokens that one CTA adds up (fp32
+// outputs: 4.3e-7 of the norm behind 2048 tokens, 9.3e-6 for 64 sequences behind 131072;
+// eager fp32: 7.9e-7, 8.5e-6).
 //
 // Three launches (programmatic dependent launch between them):
 //  1. prep: query rows into fp16 operand images (swizzled), the work schedule;
@@ -1150,11 +1154,12 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
   uint32_t ksteps = 0;
   int q0 = 0;
   bool both = false;  // the segment's queries are in both slots
+  const uint32_t stall_at = p.stall_cycles > 0 ? blockIdx.x & 7 : 0xffffffffu;
   bool more = true;
 #pragma unroll 1
   for (uint32_t k = 0, issued = 0, done = 0;; ++k) {
     const int s = k & 1;
-    if (p.stall_cycles > 0 && k == (blockIdx.x & 7)) {  // test hook: a wait that runs out
+    if (k == stall_at) {  // test hook: a wait that runs out
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sm.stall, 0, p.stall_cycles)))
         *(volatile int*)&sm.fail = 1;
       return;
@@ -1221,15 +1226,18 @@ __device__ __forceinline__ void mma_role(const PrefixParams& p, MainSmem& sm, co
       tc_fence_after();
       if (elected) {
         const uint32_t d = tmem + kColS + 128 * s, kt = kd + st * kTileD;
+        // every step drops what falls below the sum's last bit, so the small terms come
+        // first: low parts, then the narrow blocks (a plan's order is widest first)
+        const uint32_t last = ksteps - 1, ol = (last >> 2) * kPanelD + (last & 3) * 2;
 #pragma unroll 1
-        for (int part = 0; part < (q.shared ? 1 : 2); ++part) {
+        for (int part = q.shared ? 0 : 1; part >= 0; --part) {
           const uint32_t a = qd + (both ? (q.shared ? q.j & 1 : part) * kTileD
                                         : q0 * kTileD + part * (kSlotLow >> 4));
-          if (part == 0) mma_ss<false>(d, a, kt, kIdesc);
-          else mma_ss<true>(d, a, kt, kIdesc);
+          if (part || q.shared) mma_ss<false>(d, a + ol, kt + ol, kIdesc);
+          else mma_ss<true>(d, a + ol, kt + ol, kIdesc);
 #pragma unroll
-          for (uint32_t ks = 1; ks < 8; ++ks)
-            if (ks < ksteps) {
+          for (int ks = 6; ks >= 0; --ks)
+            if (ks < (int)last) {
               const uint32_t o = (ks >> 2) * kPanelD + (ks & 3) * 2;
               mma_ss<true>(d, a + o, kt + o, kIdesc);
             }

@@ -743,7 +743,7 @@ KVQ_API int kvq_paged_append_ragged(const kvq_cfg* cfg, const void* const* plans
  *        sum |q_i k_i| / sqrt(128) of itself. Ask for KVQ_FP32 outputs where that
  *        matters. An fp32 output is good to about 1e-6 of its norm for contexts of
  *        some thousand tokens; sums over long ones lose up to 2^-23 per 16 tokens
- *        that one CTA adds up (1.2e-5 measured for 64 sequences behind 131072).
+ *        that one CTA adds up (9e-6 measured for 64 sequences behind 131072).
  * ws_dev: >= kvq_prefix_decode_workspace_bytes(...) bytes, 256-byte aligned;
  *        contents overwritten, no initial value; calls that overlap on the GPU
  *        need workspaces of their own.

@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 import torch
 
+import synth
 from test_gpu_prefix_decode import DEV, U, Setup, contiguous
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +88,42 @@ def test_fp32_outputs(rows):
         num += np.sum((got[b, g] - ref) ** 2)
         den += np.sum(ref ** 2)
     assert np.sqrt(num / den) <= 2e-6, np.sqrt(num / den)
+
+
+@pytest.mark.parametrize("lead,n", [(7.6, 2000), (4.0, 55), (10.0, 20000)])
+def test_logits_are_not_shrunk(lead, n):
+    """One heavy token against n - 1 light ones of about the same weight together, their
+    values orthogonal: the ratio of the two parts of an fp32 output is the heavy
+    logit's, whatever the sums of values lose in common.
+
+    The mean of its error over 64 rows is what the products lose to truncation: a step
+    at most 2^-23 of the sum so far. With the small terms first (low parts, then the
+    blocks by energy) the sums before the last step are together at most the logit s
+    itself, so 2 * 2^-23 s; the remaining roundings (2^-22 s each, either sign) average
+    to an eighth of that, twice over; 2^-22 (s + 2) in all."""
+    S = Setup(73, 1, 4, 4)
+    sig = np.sqrt(np.concatenate([S.E[0], S.E[0]]) / 2)
+    sig /= np.linalg.norm(sig)
+    u = S.rng.standard_normal(128) * sig
+    u /= np.linalg.norm(u)
+    k = 0.02 * S.rng.standard_normal((n, 128)) * sig
+    k[0] = lead * u
+    a, b = S.rng.standard_normal((2, 128))
+    b -= a * (a @ b) / (a @ a)
+    v = np.tile(b, (n, 1))
+    v[0] = a
+    data = synth.to_bf16_bits(k[:, None]), synth.to_bf16_bits(v[:, None])
+    q = np.sqrt(128) * u * (1 + 0.1 * S.rng.standard_normal((4, 16, 1)))
+    q = torch.from_numpy(q + 0.1 * S.rng.standard_normal((4, 16, 128))).float()
+    P, Q = contiguous(S, [n], [data]), contiguous(S, [0] * 4, [([], [])] * 4, extra=8)
+    gs = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    got = Q.decode_prefix(q.to(DEV), P, gs).double().cpu().numpy()
+    kh, vh = S.heads(*data)[0]
+    parts = np.linalg.pinv(np.stack([vh[0], vh[1]], axis=1))
+    errs, s0 = [], []
+    for x, o in zip(q.double().numpy().reshape(-1, 128), got.reshape(-1, 128)):
+        s = kh @ x / np.sqrt(128)
+        heavy, light = parts @ o
+        errs.append(np.log(heavy / light) - (s[0] - np.log(np.exp(s[1:]).sum())))
+        s0.append(s[0])
+    assert abs(np.mean(errs)) <= 2.0 ** -22 * (np.mean(s0) + 2), (np.mean(errs), np.mean(s0))
