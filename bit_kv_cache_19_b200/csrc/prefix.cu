@@ -49,14 +49,15 @@
 //     one gives the streams alternate tiles. TMEM: S of both streams (P
 //     overwrites it) and O of both, 512 columns.
 //  3. combine: merges each row's records, undoes the value rotation.
-// What bounds it: no unit is near its peak. Tensor memory is full, so a stream's
-// P overwrites its S and its products and softmax take turns; that chain takes
-// about 4000 cycles per 128-token tile at few rows and 6500 to 7000 at 256 rows
-// (exponentials and tensor cores: 2048 each at their peak rates). Measured: 64
-// sequences behind one prefix of 131072 tokens, 16 query heads on 2 KV heads, K3V3:
-// 153 us, 455 TFLOP/s of useful products; 48 sequences over three prefixes (32 on 8
-// heads, K2V2, 14.4 MB): 57 us, of which main 45, prep and combine 7 each. There 37 %
-// of issue slots and 16 % of the tensor pipe's cycles are used.
+// What bounds it: no unit is near its peak, but the chain of a tile. A stream has one
+// region of 128 columns for S and P, so Q K^T, softmax and P V take turns: about 4000
+// cycles per 128-token tile at few rows (a softmax of 16 rows or fewer is one warp's
+// work) and 6500 to 7000 at 256 rows (exponentials and tensor cores: 2048 each at their
+// peak rates). Two halves of 64 tokens would fit the region and overlap; not built.
+// Measured: 64 sequences behind one prefix of 131072 tokens, 16 query heads on 2 KV
+// heads, K3V3: 154 us, 452 TFLOP/s of useful products; 48 sequences over three prefixes
+// (32 on 8 heads, K2V2, 14.4 MB): 59 us. There 36 % of main's issue slots and 19 % of
+// the tensor pipe's cycles are used; prep and combine take about 7 us each.
 #include <algorithm>
 #include <cstddef>
 
@@ -93,7 +94,8 @@ constexpr uint32_t kColS = 0, kColO = 256;
 // to leave the tile's largest P at 2^kPSet
 constexpr float kPTop = 15.f, kPSet = 7.f;
 // cost of a segment's start and of one tile (shared: 256 rows; else <= 128), near
-// the measured 4.6k to 5.3k, 6.5k to 7k and 4k cycles; 4 : 6 for the tiles and 5 for
+// the cycles measured before queries were pairs (which add 256 tensor cycles to a tile
+// of few rows): 4.6k to 5.3k, 6.5k to 7k and 4k; 4 : 6 for the tiles and 5 for
 // the start took 153 us instead of 150 for a 131072-token prefix
 constexpr int kCostSeg = 3, kCostShared = 5, kCostAlt = 3;
 constexpr int kDescs = 4;  // segments in flight

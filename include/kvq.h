@@ -746,7 +746,20 @@ KVQ_API int kvq_paged_append_ragged(const kvq_cfg* cfg, const void* const* plans
  *        that one CTA adds up (9e-6 measured for 64 sequences behind 131072).
  * ws_dev: >= kvq_prefix_decode_workspace_bytes(...) bytes, 256-byte aligned;
  *        contents overwritten, no initial value; calls that overlap on the GPU
- *        need workspaces of their own.
+ *        need workspaces of their own. Most of it are 64 KB of query rows and
+ *        132 KB of partial results for each (KV head, prefix that can have a
+ *        sequence) and each 128 rows: 32 MiB for 48 sequences behind 3 prefixes
+ *        (32 heads on 8), 444 MiB for 256 behind 256. Allocate it once.
+ * When to use it: the alternative is kvq_paged_decode_attn over rows that hold
+ * the prefix's pages and the sequence's own, which reads the prefix once per
+ * sequence. Measured on a B200 (16 heads on 2 and 32 on 8, prefixes of 512 to
+ * 131072 tokens, 1 to 64 sequences each, 32 to 2048 own tokens), this call is the
+ * faster one from about
+ *   (sequences - 2) * prefix tokens * n_kv_heads
+ *       > 400000 + own tokens of all sequences * n_kv_heads
+ * on: never for one or two sequences, at 8 sequences from 8K (8 KV heads) to 32K (2)
+ * tokens, at 64 from 1K to 4K; 64 behind 131072 tokens take a seventh to a
+ * fifteenth of the time.
  * n_prefixes 1..1024. Three launches; results do not depend on timing (the same
  * bits on every run). Other flags as for kvq_paged_decode_attn.
  */
