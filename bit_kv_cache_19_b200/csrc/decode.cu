@@ -1306,7 +1306,6 @@ static cudaError_t launch_decode_nt(const DecodeParams& p, int bits_v, int batch
 // flags TIMEOUT and skips its tiles).
 static std::atomic<long long> g_stall_cycles{0};
 void set_decode_stall(long long cycles) { g_stall_cycles.store(cycles > 0 ? cycles : 0); }
-long long decode_stall() { return g_stall_cycles.load(); }
 // Deterministic mode: the last split merges every split record in split
 // order instead of summing exponent buckets filled by L2 atomics in arrival
 // order, so outputs repeat bit for bit (slower: one CTA reads all records).

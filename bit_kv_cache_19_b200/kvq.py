@@ -346,19 +346,20 @@ def make_pages(pool, block_table, n_pages, page_tiles):
     """kvq_pages over a device pool (n_pages pages of page_bytes) and a device
     block table int32 [batch, max_pages]."""
     import torch
-    dev = pool.get_device()
-    _need(block_table, "block_table", torch.int32, (block_table.shape[0], block_table.shape[-1]),
-          dev)
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or \
+            not block_table.is_contiguous():
+        raise KVQError(ERR_ARG, f"block_table: contiguous int32 [batch, max_pages], not "
+                                f"{block_table.dtype} {tuple(block_table.shape)}")
     pages = Pages(pool.data_ptr(), block_table.data_ptr(), n_pages, page_tiles,
                   block_table.shape[1])
     # for the checks of the calls that follow the table: its rows, and the bytes
     # that the pool has for a tile's records of all KV heads
     pages.rows, pages.tile_room = block_table.shape[0], pool.nbytes // max(n_pages * page_tiles, 1)
-    pages.device = dev
+    pages.devices = {pool.get_device(), block_table.get_device()}
     return pages
 
 
-def _pages(cfg, pages, name, rows, dev):
+def _pages(cfg, pages, name, rows, dev=None):
     """Refuse a block table of fewer rows than the call's sequences, a pool
     shorter than its pages, or either on another device than the call's tensors
     (make_pages; a bare Pages says none of it)."""
@@ -367,14 +368,14 @@ def _pages(cfg, pages, name, rows, dev):
     need = cfg.n_kv_heads * (512 * (cfg.bits_k + cfg.bits_v) + 128)
     if getattr(pages, "tile_room", need) < need:
         raise KVQError(ERR_ARG, f"{name}: pool of {pages.tile_room} bytes a tile for {need}")
-    if getattr(pages, "device", dev) != dev:
-        raise KVQError(ERR_ARG, f"{name}: on device {pages.device}, lengths on device {dev}")
+    if dev is not None and getattr(pages, "devices", {dev}) != {dev}:
+        raise KVQError(ERR_ARG, f"{name}: on devices {pages.devices}, lengths on device {dev}")
 
 
 def paged_quantize_append(cfg, plan_ptrs, k, v, pages, lens, status, rope_base=0.0):
     """kvq_quantize_append into paged caches (rope_base > 1: pre-RoPE keys)."""
     batch, n_new = k.shape[0], k.shape[1]
-    _pages(cfg, pages, "pages", batch, lens.get_device())
+    _pages(cfg, pages, "pages", batch)
     _check(lib().kvq_paged_quantize_append(ctypes.byref(cfg), _ptr(plan_ptrs), _ptr(k), _ptr(v),
                                            _dtype_code(k), batch, n_new, ctypes.byref(pages),
                                            _ptr(lens), float(rope_base), _ptr(status),
@@ -384,7 +385,7 @@ def paged_quantize_append(cfg, plan_ptrs, k, v, pages, lens, status, rope_base=0
 def paged_decode_attn(cfg, plan_ptrs, pages, lens, max_len, q, out, ws, status):
     """kvq_decode_attn over paged caches."""
     batch, n_q = q.shape[0], q.shape[1]
-    _pages(cfg, pages, "pages", batch, lens.get_device())
+    _pages(cfg, pages, "pages", batch)
     _check(lib().kvq_paged_decode_attn(ctypes.byref(cfg), _ptr(plan_ptrs), ctypes.byref(pages),
                                        _ptr(lens), batch, max_len, _ptr(q), _dtype_code(q), n_q,
                                        _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
@@ -394,7 +395,7 @@ def paged_decode_attn(cfg, plan_ptrs, pages, lens, max_len, q, out, ws, status):
 def paged_decode_attn_partial(cfg, plan_ptrs, pages, lens, max_len, q, rec, ws, status):
     """kvq_decode_attn_partial over paged caches: records fp32 [batch, n_q, 132]."""
     batch, n_q = q.shape[0], q.shape[1]
-    _pages(cfg, pages, "pages", batch, lens.get_device())
+    _pages(cfg, pages, "pages", batch)
     _check(lib().kvq_paged_decode_attn_partial(ctypes.byref(cfg), _ptr(plan_ptrs),
                                                ctypes.byref(pages), _ptr(lens), batch, max_len,
                                                _ptr(q), _dtype_code(q), n_q, _ptr(rec), _ptr(ws),
@@ -407,7 +408,7 @@ def paged_append_decode(cfg, plan_ptrs, k, v, pages, lens, max_len, q, out, ws, 
     """kvq_append_decode over paged caches."""
     batch, n_q = q.shape[0], q.shape[1]
     n_new = 0 if k is None else k.shape[1]
-    _pages(cfg, pages, "pages", batch, lens.get_device())
+    _pages(cfg, pages, "pages", batch)
     _check(lib().kvq_paged_append_decode(ctypes.byref(cfg), _ptr(plan_ptrs), _ptr(k), _ptr(v),
                                          _dtype_code(k) if k is not None else BF16, n_new,
                                          ctypes.byref(pages), _ptr(lens), batch, max_len,
@@ -518,15 +519,14 @@ class _Dtypes(dict):
 _DTYPES = _Dtypes()
 
 
-def _stream_of(t):
-    """The current stream of the tensor's device, which must be the current
-    device: the library launches there."""
+def _stream_of(dev):
+    """The current stream of device dev, that of the call's tensors, which must be
+    the current one: the library launches there."""
     import torch
-    i = t.get_device()
-    if i != torch.cuda.current_device():
-        raise KVQError(ERR_ARG, f"tensors on device {i}, current device "
+    if dev != torch.cuda.current_device():
+        raise KVQError(ERR_ARG, f"tensors on device {dev}, current device "
                                 f"{torch.cuda.current_device()}")
-    return torch._C._cuda_getCurrentRawStream(i)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _need(t, name, dtype, shape, dev):
@@ -595,7 +595,7 @@ def pages_assign(state, lens, n_new, cu, slots, pos, ws, status):
         raise KVQError(ERR_ARG, f"tensors on device {dev}, page state on device {state.device}")
     rc = lib().kvq_pages_assign(state, lens.data_ptr(), n_new.data_ptr(), batch, n_slots,
                                 cu.data_ptr(), slots.data_ptr(), pos, ws.data_ptr(), ws.nbytes,
-                                status.data_ptr(), _stream_of(lens))
+                                status.data_ptr(), _stream_of(dev))
     if rc:
         _check(rc)
 
@@ -623,7 +623,7 @@ def paged_append_ragged(cfg, plan_ptrs, k, v, cu, slots, pool, n_pages, page_til
                                        _DTYPES[k.dtype], n_rows, cu.data_ptr(), slots.data_ptr(),
                                        batch, pool.data_ptr(), n_pages, page_tiles,
                                        lens.data_ptr(), rope_base, status.data_ptr(),
-                                       _stream_of(lens))
+                                       _stream_of(dev))
     if rc:
         _check(rc)
 
@@ -662,7 +662,7 @@ def prefix_decode_attn(cfg, plan_ptrs, prefix_ptrs, prefix_lens, group_start, ma
         group_start.data_ptr(), n_prefixes, max_prefix_len, cache_ptrs.data_ptr(),
         lens.data_ptr(), batch, max_len, q.data_ptr(), _DTYPES[q.dtype], q.shape[1],
         out.data_ptr(), _DTYPES[out.dtype], ws.data_ptr(), ws.nbytes, status.data_ptr(),
-        _stream_of(q))
+        _stream_of(dev))
     if rc:
         _check(rc)
 
@@ -679,6 +679,6 @@ def paged_prefix_decode_attn(cfg, plan_ptrs, prefix_pages, prefix_lens, group_st
         cfg, plan_ptrs.data_ptr(), prefix_pages, prefix_lens.data_ptr(), group_start.data_ptr(),
         n_prefixes, max_prefix_len, pages, lens.data_ptr(), batch, max_len, q.data_ptr(),
         _DTYPES[q.dtype], q.shape[1], out.data_ptr(), _DTYPES[out.dtype], ws.data_ptr(),
-        ws.nbytes, status.data_ptr(), _stream_of(q))
+        ws.nbytes, status.data_ptr(), _stream_of(dev))
     if rc:
         _check(rc)

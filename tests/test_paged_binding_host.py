@@ -70,6 +70,21 @@ def test_short_block_tables_and_pools_are_refused(call, no_call):
         _calls(kvq.Pages(16, 16, 5, 4, 6), kvq.Pages(16, 16, 5, 4, 6))[call]()
 
 
+@pytest.mark.parametrize("call", ["append", "decode", "partial", "step"])
+def test_lengths_in_mapped_host_memory_still_go_through(call, no_call, monkeypatch):
+    """The calls over plain block tables take lengths, tables and pools at any address
+    the GPU can read."""
+    host = kvq.make_pages(torch.zeros(5 * PAGE, dtype=torch.uint8),
+                          torch.zeros(3, 6, dtype=torch.int32), 5, 4)
+    with pytest.raises(AssertionError, match="the library was called"):
+        _calls(host, host)[call]()
+    monkeypatch.setattr(OnGpu, "get_device", lambda self: self.where if self.tensor.dim() != 1
+                        or len(self.tensor) != 3 else -1)
+    pages = _pages(3)
+    with pytest.raises(AssertionError, match="the library was called"):
+        _calls(pages, pages)[call]()
+
+
 def test_short_prefix_table_is_refused(no_call):
     with pytest.raises(kvq.KVQError, match="prefix_pages: block table of 1 rows for 2"):
         _calls(_pages(3), _pages(1))["prefix"]()
@@ -82,8 +97,15 @@ def test_short_prefix_table_is_refused(no_call):
 def test_block_table_of_another_kind_is_refused(table):
     with pytest.raises(kvq.KVQError, match="block_table"):
         kvq.make_pages(OnGpu(torch.zeros(5 * PAGE)), OnGpu(table), 5, 4)
-    with pytest.raises(kvq.KVQError, match="block_table"):  # host memory
-        kvq.make_pages(torch.zeros(5 * PAGE), torch.zeros(3, 6, dtype=torch.int32), 5, 4)
+
+
+def test_prefix_call_refuses_pages_in_host_memory(no_call):
+    args = _arguments(0)
+    for name in ("pool", "table", "prefix_table"):
+        args[name] = _arguments(0)[name].tensor
+        with pytest.raises(kvq.KVQError, match="pages: on devices"):
+            _paged_prefix(args)
+        args[name] = _arguments(0)[name]
 
 
 def _arguments(device):
@@ -168,5 +190,5 @@ def test_all_page_state_on_another_gpu_is_refused(no_call):
     args = _arguments(0)
     for name in ("pool", "table", "prefix_table"):
         args[name] = _arguments(1)[name]
-    with pytest.raises(kvq.KVQError, match="on device 1, lengths on device 0"):
+    with pytest.raises(kvq.KVQError, match=r"on devices \{1\}, lengths on device 0"):
         _paged_prefix(args)
