@@ -638,6 +638,7 @@ int kvq_combine_partials(const kvq_cfg* cfg, const void* const* plans_dev, int n
 int kvq_debug_decode_stall(long long cycles) {
   if (cycles < 0 || cycles > (1ll << 40)) return fail(KVQ_ERR_ARG, "stall cycles %lld", cycles);
   set_decode_stall(cycles);
+  set_prefix_stall(cycles);
   return KVQ_OK;
 }
 

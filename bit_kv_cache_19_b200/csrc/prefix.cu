@@ -59,6 +59,7 @@
 // (32 on 8 heads, K2V2, 14.4 MB): 59 us. There 36 % of main's issue slots and 19 % of
 // the tensor pipe's cycles are used; prep and combine take about 7 us each.
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 
 #include "prefix.cuh"
@@ -1797,6 +1798,10 @@ static cudaError_t launch_all(const PrefixParams& p, cudaStream_t st) {
                     (size_t)(p.n_ctas + 1) * sizeof(int64_t), p, parts);
 }
 
+// Test hook: > 0 makes the warp that issues the products give up after so long a wait.
+static std::atomic<long long> g_stall_cycles{0};
+void set_prefix_stall(long long cycles) { g_stall_cycles.store(cycles > 0 ? cycles : 0); }
+
 cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes, cudaStream_t st) {
   cudaError_t e;
   PrefixParams p;
@@ -1811,7 +1816,7 @@ cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes,
   // a query operand of two terms leaves no room for a second row tile: 256 rows to a
   // unit only where the queries come with bf16's 8 bits (see the top of the file)
   p.rows_unit = split || a.q_dtype != KVQ_BF16 ? 128 : 256;
-  p.stall_cycles = decode_stall();
+  p.stall_cycles = g_stall_cycles.load();
   uint8_t* const s = static_cast<uint8_t*>(ws);
   p.head = reinterpret_cast<PfxHead*>(s + w.head);
   p.cuts = reinterpret_cast<int64_t*>(s + w.cuts);

@@ -26,7 +26,7 @@ struct PrefixArgs {
 };
 
 size_t prefix_workspace_bytes(int batch, int n_q, int n_kv, int n_groups);
-long long decode_stall();  // kvq_debug_decode_stall's cycles (decode.cu)
+void set_prefix_stall(long long cycles);  // kvq_debug_decode_stall
 cudaError_t launch_prefix_decode(const PrefixArgs& a, void* ws, size_t ws_bytes, cudaStream_t st);
 
 }  // namespace kvq
